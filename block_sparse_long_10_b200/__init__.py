@@ -30,6 +30,10 @@ __all__ = [
     "qsa_index_distill", "qsa_index_distill_workspace_size", "qsa_sparse_attn_backward",
     "qsa_gdn_prefill", "qsa_gdn_decode", "qsa_gdn_prefill_chunked",
     "qsa_gdn_prefill_chunked_workspace_size", "qsa_probe_l2_read",
+    "qsa_rope_frequencies", "qsa_rope", "qsa_qk_norm_rope", "qsa_qk_norm_rope_backward",
+    "qsa_qk_norm_rope_backward_workspace_size",
+    "qsa_dense_tree_decode", "qsa_dense_tree_decode_workspace_size",
+    "qsa_sparse_tree_decode", "qsa_sparse_tree_decode_workspace_size",
     "qsa_check_device_status", "qsa_status_string", "qsa_version",
 ]
 
@@ -56,6 +60,7 @@ def lib_path() -> str:
 
 _VP, _I, _I64, _F, _SZ = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
                           ctypes.c_float, ctypes.c_size_t)
+_D = ctypes.c_double
 _SIGS = {
     "qsa_pool": (_I, [_VP, _I, _I64, _I, _I, _I64, _I64, _VP, _VP]),
     "qsa_index_topk_workspace_size": (_SZ, [_I, _I64, _I64, _I, _I, _I, _I]),
@@ -92,6 +97,21 @@ _SIGS = {
     "qsa_index_distill_sparse": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I64, _I, _I, _I,
                                       _I, _I, _I, _I, _F, _VP, _VP, _VP, _VP, _VP, _VP, _SZ,
                                       _VP]),
+    "qsa_rope_frequencies": (_I, [_D, _I, _I, _D, _D, _D, _D, _VP, _VP]),
+    "qsa_rope": (_I, [_VP, _I64, _VP, _I64, _I, _I, _I64, _I, _I, _VP, _I, _I, _F, _I, _VP, _VP,
+                      _VP]),
+    "qsa_qk_norm_rope": (_I, [_VP, _I64, _VP, _I64, _VP, _I64, _I, _I64, _I, _I, _I, _VP, _VP, _F,
+                              _VP, _I, _I, _F, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP, _VP]),
+    "qsa_qk_norm_rope_backward_workspace_size": (_SZ, [_I, _I64, _I, _I, _I]),
+    "qsa_qk_norm_rope_backward": (_I, [_VP, _VP, _I, _VP, _I64, _VP, _I64, _I, _I64, _I, _I, _I,
+                                       _VP, _VP, _F, _VP, _I, _I, _F, _VP, _VP, _VP, _VP, _I,
+                                       _VP, _VP, _VP, _SZ, _VP]),
+    "qsa_dense_tree_decode_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "qsa_dense_tree_decode": (_I, [_VP, _VP, _VP, _VP, _I64, _VP, _VP, _I, _I, _I, _I, _I, _F,
+                                   _VP, _VP, _VP, _SZ, _VP]),
+    "qsa_sparse_tree_decode_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "qsa_sparse_tree_decode": (_I, [_VP, _VP, _VP, _VP, _I64, _VP, _I64, _I64, _VP, _VP, _I, _I,
+                                    _I, _I, _I, _I, _I, _F, _VP, _VP, _VP, _SZ, _VP]),
     "qsa_check_device_status": (_I, [_VP, _VP]),
     "qsa_status_string": (ctypes.c_char_p, [_I]),
     "qsa_version": (ctypes.c_char_p, []),
@@ -466,6 +486,254 @@ def qsa_index_distill_sparse(q, k, lse, sel, q_idx, w, k_pooled, kl, dq_idx, dw,
           _ptr(w), _ptr(k_pooled), B, T, Hq, Hkv, D, Hi, Di, r, budget, scale, _ptr(kl),
           _ptr(dq_idx), _ptr(dw), _ptr(dk_pooled), _ptr(dk_idx), _ptr(ws), ws.numel(),
           _stream(stream, q.device))
+
+
+# ------------------------------------------ rotary positions, per-head norms --
+
+_LAYOUT = {"half": 0, "interleaved": 1}
+_SCALING = {"none": 0, "linear": 1, "ntk": 2, "by-parts": 3}
+_DTYPE = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _shape(t, shape, name):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _rows(t, dtype, name, shape=None):
+    """A [B,T,H,D] CUDA tensor whose tokens lie at one stride, heads packed; the stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 4:
+        raise ValueError(f"{name} must have 4 dims, got {tuple(t.shape)}")
+    if shape is not None:
+        _shape(t, shape, name)
+    B, T, H, D = t.shape
+    sb, st, sh, sd = t.stride()
+    if T == 1:
+        st = sb if B > 1 else H * D
+    if (D > 1 and sd != 1) or (H > 1 and sh != D) or (B > 1 and T > 0 and sb != T * st):
+        raise ValueError(f"{name}'s tokens must lie at one stride, its heads packed; "
+                         f"strides {t.stride()}")
+    return max(st, H * D) if B * T <= 1 else st
+
+
+def _layout(layout):
+    if layout not in _LAYOUT:
+        raise ValueError(f"layout must be one of {sorted(_LAYOUT)}, got {layout!r}")
+    return _LAYOUT[layout]
+
+
+def _one_device(first, **others):
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
+
+
+def _call_on(device, name, *args):
+    """_call with `device` current: the library launches on the current device."""
+    if torch.cuda.current_device() == device.index:
+        _call(name, *args)
+    else:
+        with torch.cuda.device(device):
+            _call(name, *args)
+
+
+def qsa_rope_frequencies(base, rot, scaling="none", factor=1.0, orig_len=0.0, beta_fast=32.0,
+                         beta_slow=1.0, device=None):
+    """(freq [rot/2] fp64 on `device` (default: the host), mscale): rotary frequencies
+    in radians per position and the factor on rotated dims, plain or stretched for
+    contexts longer than orig_len ("linear", "ntk", "by-parts")."""
+    if scaling not in _SCALING:
+        raise ValueError(f"scaling must be one of {sorted(_SCALING)}, got {scaling!r}")
+    freq = torch.empty(max(int(rot), 2) // 2, dtype=torch.float64)
+    mscale = ctypes.c_float(1.0)
+    _call("qsa_rope_frequencies", float(base), int(rot), _SCALING[scaling], float(factor),
+          float(orig_len), float(beta_fast), float(beta_slow), _ptr(freq), ctypes.byref(mscale))
+    return (freq if device is None else freq.to(device)), mscale.value
+
+
+def _positions(pos, pos0, B, T):
+    _need(pos, _I64T, "pos", 2)
+    _need(pos0, _I64T, "pos0", 1)
+    _shape(pos, (B, T), "pos")
+    _shape(pos0, (B,), "pos0")
+
+
+def _freq(freq):
+    """(pointer, rot) of a frequency table; None: no rotation."""
+    if freq is None:
+        return None, 0
+    _need(freq, torch.float64, "freq", 1)
+    return _ptr(freq), 2 * freq.numel()
+
+
+def qsa_rope(x, y, freq, pos=None, pos0=None, layout="half", mscale=1.0, transpose=False,
+             stream=None):
+    """x [B,T,H,D] bf16 or fp32 -> y (same type; may be x): the first 2 * len(freq) dims of
+    each head turned by position * freq; transpose: the gradient's map.  Tokens may lie at
+    any one stride (a part of a packed projection), heads packed."""
+    if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPE:
+        raise TypeError("x must be a torch.bfloat16 or torch.float32 tensor")
+    xs = _rows(x, x.dtype, "x")
+    ys = _rows(y, x.dtype, "y", x.shape)
+    B, T, H, D = x.shape
+    fp, rot = _freq(freq)
+    _positions(pos, pos0, B, T)
+    _one_device(x, y=y, freq=freq, pos=pos, pos0=pos0)
+    _call_on(x.device, "qsa_rope", _ptr(x), xs, _ptr(y), ys, _DTYPE[x.dtype], B, T, H, D, fp, rot,
+             _layout(layout), mscale, int(bool(transpose)), _ptr(pos), _ptr(pos0),
+             _stream(stream, x.device))
+
+
+def qsa_qk_norm_rope(q, k, q_out, k_out, freq, v=None, v_out=None, q_weight=None, k_weight=None,
+                     eps=1e-6, pos=None, pos0=None, layout="half", mscale=1.0, slot=None, ws=None,
+                     stream=None):
+    """q [B,T,Hq,D], k/v [B,T,Hkv,D] bf16 -> q_out [B,T,Hq,D], k_out/v_out [B,T,Hkv,D], or
+    with slot [B,T] int64 the rows slot of caches [B,L,Hkv,D]: per-head RMS norm (where a
+    weight [D] fp32 is given), then the rotation; v is copied.  Inputs may be parts of one
+    packed projection.  ws: takes the status word (a slot >= L)."""
+    qs = _rows(q, _BF, "q")
+    ks = _rows(k, _BF, "k")
+    B, T, Hq, D = q.shape
+    Hkv = k.shape[2]
+    _shape(k, (B, T, Hkv, D), "k")
+    vs = 0 if v is None else _rows(v, _BF, "v", k.shape)
+    if (v is None) != (v_out is None):
+        raise ValueError("v and v_out go together")
+    _need(q_out, _BF, "q_out", 4)
+    _shape(q_out, q.shape, "q_out")
+    _need(k_out, _BF, "k_out", 4)
+    L = k_out.shape[1]
+    _shape(k_out, (B, T if slot is None else L, Hkv, D), "k_out")
+    _need(v_out, _BF, "v_out", 4)
+    _shape(v_out, k_out.shape, "v_out")
+    _need(q_weight, _F32, "q_weight", 1)
+    _need(k_weight, _F32, "k_weight", 1)
+    _shape(q_weight, (D,), "q_weight")
+    _shape(k_weight, (D,), "k_weight")
+    _need(slot, _I64T, "slot", 2)
+    _shape(slot, (B, T), "slot")
+    _need(ws, torch.uint8, "ws", 1)
+    if ws is not None and ws.numel() < 256:
+        raise ValueError("ws must hold the 256-byte status header")
+    fp, rot = _freq(freq)
+    _positions(pos, pos0, B, T)
+    _one_device(q, k=k, v=v, q_out=q_out, k_out=k_out, v_out=v_out, q_weight=q_weight,
+                k_weight=k_weight, freq=freq, pos=pos, pos0=pos0, slot=slot, ws=ws)
+    _call_on(q.device, "qsa_qk_norm_rope", _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, B, T, Hq, Hkv,
+             D, _ptr(q_weight), _ptr(k_weight), eps, fp, rot, _layout(layout), mscale, _ptr(pos),
+             _ptr(pos0), _ptr(q_out), _ptr(k_out), _ptr(v_out), _ptr(slot), L, _ptr(ws),
+             _stream(stream, q.device))
+
+
+def qsa_qk_norm_rope_backward_workspace_size(B, T, Hq, Hkv, D) -> int:
+    return _size("qsa_qk_norm_rope_backward_workspace_size", B, T, Hq, Hkv, D)
+
+
+def qsa_qk_norm_rope_backward(d_q, d_k, q, k, dq, dk, freq, ws=None, q_weight=None, k_weight=None,
+                              dq_weight=None, dk_weight=None, eps=1e-6, pos=None, pos0=None,
+                              layout="half", mscale=1.0, stream=None):
+    """Gradients d_q [B,T,Hq,D], d_k [B,T,Hkv,D] (bf16 or fp32) of qsa_qk_norm_rope's outputs
+    -> dq, dk (bf16 or fp32) of its inputs q, k, and dq_weight, dk_weight [D] fp32 of its
+    weights (overwritten), where wanted; ws: for the weight gradients."""
+    for t, n in ((d_q, "d_q"), (dq, "dq")):
+        if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPE:
+            raise TypeError(f"{n} must be a torch.bfloat16 or torch.float32 tensor")
+    qs = _rows(q, _BF, "q")
+    ks = _rows(k, _BF, "k")
+    B, T, Hq, D = q.shape
+    Hkv = k.shape[2]
+    _shape(k, (B, T, Hkv, D), "k")
+    for t, ref, dt, n in ((d_q, q, d_q.dtype, "d_q"), (d_k, k, d_q.dtype, "d_k"),
+                          (dq, q, dq.dtype, "dq"), (dk, k, dq.dtype, "dk")):
+        _need(t, dt, n, 4)
+        _shape(t, ref.shape, n)
+    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight"), (dq_weight, "dq_weight"),
+                 (dk_weight, "dk_weight")):
+        _need(t, _F32, n, 1)
+        _shape(t, (D,), n)
+    _need(ws, torch.uint8, "ws", 1)
+    fp, rot = _freq(freq)
+    _positions(pos, pos0, B, T)
+    _one_device(q, d_q=d_q, d_k=d_k, k=k, dq=dq, dk=dk, q_weight=q_weight, k_weight=k_weight,
+                dq_weight=dq_weight, dk_weight=dk_weight, freq=freq, pos=pos, pos0=pos0, ws=ws)
+    _call_on(q.device, "qsa_qk_norm_rope_backward", _ptr(d_q), _ptr(d_k), _DTYPE[d_q.dtype],
+             _ptr(q), qs, _ptr(k), ks, B, T, Hq, Hkv, D, _ptr(q_weight), _ptr(k_weight), eps, fp,
+             rot, _layout(layout), mscale, _ptr(pos), _ptr(pos0), _ptr(dq), _ptr(dk),
+             _DTYPE[dq.dtype], _ptr(dq_weight), _ptr(dk_weight), _ptr(ws),
+             0 if ws is None else ws.numel(), _stream(stream, q.device))
+
+
+# ------------------------------------------------ trees of drafted tokens --
+
+def _tree(q, k_cache, v_cache, seqlens, parent, o, ws, n_draft, lse):
+    _need(q, _BF, "q", 4)
+    _need(k_cache, _BF, "k_cache", 4)
+    _need(v_cache, _BF, "v_cache", 4)
+    _need(o, _BF, "o", 4)
+    _need(seqlens, _I32, "seqlens", 1)
+    _need(parent, _I32, "parent", 2)
+    _need(n_draft, _I32, "n_draft", 1)
+    _need(lse, _F32, "lse", 3)
+    _need(ws, torch.uint8, "ws", 1)
+    B, N, Hq, D = q.shape
+    L, Hkv = k_cache.shape[1], k_cache.shape[2]
+    _shape(k_cache, (B, L, Hkv, D), "k_cache")
+    _shape(v_cache, k_cache.shape, "v_cache")
+    _shape(o, q.shape, "o")
+    _shape(seqlens, (B,), "seqlens")
+    _shape(parent, (B, N), "parent")
+    _shape(n_draft, (B,), "n_draft")
+    _shape(lse, (B, N, Hq), "lse")
+    _one_device(q, k_cache=k_cache, v_cache=v_cache, seqlens=seqlens, parent=parent, o=o, ws=ws,
+                n_draft=n_draft, lse=lse)
+    return B, N, Hq, Hkv, D, L
+
+
+def qsa_dense_tree_decode_workspace_size(B, N, Hq, Hkv, D) -> int:
+    return _size("qsa_dense_tree_decode_workspace_size", B, N, Hq, Hkv, D)
+
+
+def qsa_dense_tree_decode(q, k_cache, v_cache, seqlens, parent, o, ws, n_draft=None, scale=None,
+                          lse=None, stream=None):
+    """Drafted tokens q [B,N,Hq,D], the last n_draft[b] (default N) of the seqlens[b] rows of
+    caches [B,L,Hkv,D], over the whole prefix and each over its chain of parents [B,N]
+    (-1: the last committed token) -> o [B,N,Hq,D]."""
+    B, N, Hq, Hkv, D, L = _tree(q, k_cache, v_cache, seqlens, parent, o, ws, n_draft, lse)
+    scale = D ** -0.5 if scale is None else scale
+    _call_on(q.device, "qsa_dense_tree_decode", _ptr(q), _ptr(k_cache), _ptr(v_cache),
+             _ptr(seqlens), L, _ptr(parent), _ptr(n_draft), B, N, Hq, Hkv, D, scale, _ptr(o),
+             _ptr(lse), _ptr(ws), ws.numel(), _stream(stream, q.device))
+
+
+def qsa_sparse_tree_decode_workspace_size(B, N, Hq, D, r=4, budget=2048) -> int:
+    return _size("qsa_sparse_tree_decode_workspace_size", B, N, Hq, D, r, budget)
+
+
+def qsa_sparse_tree_decode(q, k_cache, v_cache, seqlens, sel, parent, o, ws, n_draft=None, r=4,
+                           budget=2048, scale=None, lse=None, stream=None):
+    """qsa_dense_tree_decode with each row's prefix cut to its selected blocks sel
+    [B,N,budget//r] int32 (any strides but the last; .expand shares one selection) and the
+    tokens after the last complete block."""
+    B, N, Hq, Hkv, D, L = _tree(q, k_cache, v_cache, seqlens, parent, o, ws, n_draft, lse)
+    if not isinstance(sel, torch.Tensor) or sel.dtype != _I32:
+        raise TypeError("sel must be a torch.int32 tensor")
+    if not sel.is_cuda or sel.dim() != 3:
+        raise ValueError("sel must be a CUDA tensor of 3 dims")
+    _shape(sel, (B, N, budget // r), "sel")
+    if sel.shape[2] > 1 and sel.stride(2) != 1:
+        raise ValueError("sel's entries must be contiguous")
+    _one_device(q, sel=sel)
+    scale = D ** -0.5 if scale is None else scale
+    _call_on(q.device, "qsa_sparse_tree_decode", _ptr(q), _ptr(k_cache), _ptr(v_cache),
+             _ptr(seqlens), L, _ptr(sel), sel.stride(0), sel.stride(1), _ptr(parent),
+             _ptr(n_draft), B, N, Hq, Hkv, D, r, budget, scale, _ptr(o), _ptr(lse), _ptr(ws),
+             ws.numel(), _stream(stream, q.device))
 
 
 def qsa_check_device_status(ws, stream=None) -> int:

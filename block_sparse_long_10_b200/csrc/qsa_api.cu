@@ -3,6 +3,7 @@
 // touching the CUDA runtime when an argument is wrong, so argument errors are
 // reported identically with or without a GPU.
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -463,6 +464,221 @@ qsa_status_t qsa_index_distill_sparse(const qsa_bf16_t *q, const qsa_bf16_t *k,
     return from_cuda(qsa::launch_index_distill_sparse(
         q, k, lse, sel, q_idx, w, k_pooled, B, T, Hq, Hkv, D, Hi, Di, kb, scale, kl, dq_idx, dw,
         dk_pooled, dk_idx, ws, static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------- rotary positions, per-head norms --
+
+static bool supported_head(int D) { return D == 32 || D == 64 || D == 128 || D == 256; }
+
+static bool valid_dtype(int t) { return t == QSA_BF16 || t == QSA_F32; }
+
+static bool valid_layout(int l) { return l == QSA_ROPE_HALF || l == QSA_ROPE_INTERLEAVED; }
+
+// Rows of H heads of D elements every `stride`: 0 heads never reach here.
+static bool valid_stride(int64_t stride, int H, int D, int esize) {
+    return stride >= (int64_t)H * D && stride * esize % 16 == 0;
+}
+
+static bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+qsa_status_t qsa_rope_frequencies(double base, int rot, int scaling, double factor,
+                                  double orig_len, double beta_fast, double beta_slow,
+                                  double *freq, float *mscale) {
+    if (!freq || rot < 2 || rot % 2 != 0 || !(base > 1.0) || !isfinite(base) ||
+        !(factor >= 1.0) || !isfinite(factor))
+        return QSA_ERR_INVALID_ARG;
+    if (scaling < QSA_ROPE_PLAIN || scaling > QSA_ROPE_BY_PARTS) return QSA_ERR_INVALID_ARG;
+    if (scaling == QSA_ROPE_NTK && rot < 4) return QSA_ERR_INVALID_ARG;
+    double lo = 0, hi = 0;
+    if (scaling == QSA_ROPE_BY_PARTS) {
+        if (!(orig_len > 0) || !isfinite(orig_len) || !(beta_slow > 0) ||
+            !(beta_fast >= beta_slow) || !isfinite(beta_fast))
+            return QSA_ERR_INVALID_ARG;
+        const double two_pi = 6.283185307179586476925286766559;
+        const double per = rot / (2 * log(base));
+        lo = fmax(floor(per * log(orig_len / (two_pi * beta_fast))), 0.0);
+        hi = fmin(ceil(per * log(orig_len / (two_pi * beta_slow))), (double)(rot - 1));
+    }
+    if (scaling == QSA_ROPE_NTK) base *= pow(factor, (double)rot / (rot - 2));
+    for (int i = 0; i < rot / 2; ++i) {
+        double f = pow(base, -2.0 * i / rot);
+        if (scaling == QSA_ROPE_LINEAR) f /= factor;
+        if (scaling == QSA_ROPE_BY_PARTS) {
+            const double w = fmin(fmax((i - lo) / fmax(hi - lo, 0.001), 0.0), 1.0);
+            f = f * (1 - w) + f / factor * w;
+        }
+        freq[i] = f;
+    }
+    if (mscale) *mscale = scaling == QSA_ROPE_BY_PARTS ? (float)(0.1 * log(factor) + 1.0) : 1.f;
+    return QSA_OK;
+}
+
+qsa_status_t qsa_rope(const void *x, int64_t x_stride, void *y, int64_t y_stride, int dtype,
+                      int B, int64_t T, int H, int D, const double *freq, int rot, int layout,
+                      float mscale, int transpose, const int64_t *pos, const int64_t *pos0,
+                      void *stream) {
+    if (B < 1 || T < 0 || H < 1 || D < 1 || rot < 0 || rot > D || !valid_dtype(dtype) ||
+        !valid_layout(layout) || !isfinite(mscale))
+        return QSA_ERR_INVALID_ARG;
+    if (!supported_head(D) || rot % 8 != 0) return QSA_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) return QSA_OK;
+    if (!x || !y || (rot > 0 && !freq)) return QSA_ERR_INVALID_ARG;
+    const int es = dtype == QSA_F32 ? 4 : 2;
+    if (!aligned16(x) || !aligned16(y) || !valid_stride(x_stride, H, D, es) ||
+        !valid_stride(y_stride, H, D, es) || !aligned8(freq) || !aligned8(pos) ||
+        !aligned8(pos0) || (x == y && x_stride != y_stride))
+        return QSA_ERR_INVALID_ARG;
+    int sms = 0;
+    qsa_status_t st = current_device(&sms);
+    if (st != QSA_OK) return st;
+    return from_cuda(qsa::launch_rope(x, x_stride, y, y_stride, dtype == QSA_F32, B, T, H, D,
+                                      freq, rot, layout == QSA_ROPE_HALF, mscale,
+                                      transpose != 0, pos, pos0, sms,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+qsa_status_t qsa_qk_norm_rope(const qsa_bf16_t *q, int64_t q_stride, const qsa_bf16_t *k,
+                              int64_t k_stride, const qsa_bf16_t *v, int64_t v_stride, int B,
+                              int64_t T, int Hq, int Hkv, int D, const float *q_weight,
+                              const float *k_weight, float eps, const double *freq, int rot,
+                              int layout, float mscale, const int64_t *pos, const int64_t *pos0,
+                              qsa_bf16_t *q_out, qsa_bf16_t *k_out, qsa_bf16_t *v_out,
+                              const int64_t *slot, int64_t L_max, void *ws, void *stream) {
+    if (B < 1 || T < 0 || Hq < 1 || Hkv < 1 || D < 1 || rot < 0 || rot > D ||
+        !valid_layout(layout) || !isfinite(mscale) || !(eps >= 0.f) || !isfinite(eps) ||
+        L_max < 0)
+        return QSA_ERR_INVALID_ARG;
+    if (!supported_head(D) || rot % 8 != 0) return QSA_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) return QSA_OK;
+    if (!q || !k || !q_out || (rot > 0 && !freq) || (v == nullptr) != (v_out == nullptr) ||
+        (!slot && L_max != T))
+        return QSA_ERR_INVALID_ARG;
+    if (L_max > 0 && !k_out) return QSA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) ||
+        !aligned16(k_out) || !aligned16(v_out) || !aligned16(q_weight) || !aligned16(k_weight) ||
+        !aligned8(freq) || !aligned8(pos) || !aligned8(pos0) || !aligned8(slot) ||
+        !aligned16(ws) || !valid_stride(q_stride, Hq, D, 2) ||
+        !valid_stride(k_stride, Hkv, D, 2) || (v && !valid_stride(v_stride, Hkv, D, 2)))
+        return QSA_ERR_INVALID_ARG;
+    int sms = 0;
+    qsa_status_t st = current_device(&sms);
+    if (st != QSA_OK) return st;
+    return from_cuda(qsa::launch_norm_rope(q, q_stride, k, k_stride, v, v_stride, B, T, Hq, Hkv,
+                                           D, q_weight, k_weight, eps, freq, rot,
+                                           layout == QSA_ROPE_HALF, mscale, pos, pos0, q_out,
+                                           k_out, v_out, slot, L_max, ws, sms,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+size_t qsa_qk_norm_rope_backward_workspace_size(int B, int64_t T, int Hq, int Hkv, int D) {
+    if (B < 1 || T < 0 || Hq < 1 || Hkv < 1 || !supported_head(D)) return SIZE_MAX;
+    return qsa::norm_rope_grad_ws_bytes((int64_t)B * T, Hq, Hkv, D);
+}
+
+qsa_status_t qsa_qk_norm_rope_backward(
+    const void *d_q, const void *d_k, int d_dtype, const qsa_bf16_t *q, int64_t q_stride,
+    const qsa_bf16_t *k, int64_t k_stride, int B, int64_t T, int Hq, int Hkv, int D,
+    const float *q_weight, const float *k_weight, float eps, const double *freq, int rot,
+    int layout, float mscale, const int64_t *pos, const int64_t *pos0, void *dq, void *dk,
+    int dx_dtype, float *dq_weight, float *dk_weight, void *ws, size_t ws_bytes, void *stream) {
+    if (B < 1 || T < 0 || Hq < 1 || Hkv < 1 || D < 1 || rot < 0 || rot > D ||
+        !valid_layout(layout) || !valid_dtype(d_dtype) || !valid_dtype(dx_dtype) ||
+        !isfinite(mscale) || !(eps >= 0.f) || !isfinite(eps))
+        return QSA_ERR_INVALID_ARG;
+    if ((dq_weight && !q_weight) || (dk_weight && !k_weight)) return QSA_ERR_INVALID_ARG;
+    if (!supported_head(D) || rot % 8 != 0) return QSA_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0 && !dq_weight && !dk_weight) return QSA_OK;
+    if (T > 0 && (!d_q || !d_k || !q || !k || !dq || !dk || (rot > 0 && !freq)))
+        return QSA_ERR_INVALID_ARG;
+    if ((dq_weight || dk_weight) &&
+        (!ws || !aligned16(ws) ||
+         ws_bytes < qsa::norm_rope_grad_ws_bytes((int64_t)B * T, Hq, Hkv, D)))
+        return QSA_ERR_WORKSPACE;
+    if (!aligned16(d_q) || !aligned16(d_k) || !aligned16(q) || !aligned16(k) ||
+        !aligned16(dq) || !aligned16(dk) || !aligned16(q_weight) || !aligned16(k_weight) ||
+        !aligned8(freq) || !aligned8(pos) || !aligned8(pos0) ||
+        (T > 0 && (!valid_stride(q_stride, Hq, D, 2) || !valid_stride(k_stride, Hkv, D, 2))))
+        return QSA_ERR_INVALID_ARG;
+    if (d_dtype != dx_dtype && T > 0 && (d_q == dq || d_k == dk)) return QSA_ERR_INVALID_ARG;
+    int sms = 0;
+    qsa_status_t st = current_device(&sms);
+    if (st != QSA_OK) return st;
+    return from_cuda(qsa::launch_norm_rope_grad(
+        d_q, d_k, d_dtype == QSA_F32, q, q_stride, k, k_stride, B, T, Hq, Hkv, D, q_weight,
+        k_weight, eps, freq, rot, layout == QSA_ROPE_HALF, mscale, pos, pos0, dq, dk,
+        dx_dtype == QSA_F32, dq_weight, dk_weight, ws, sms, static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------- trees of drafted tokens --
+
+static qsa_status_t check_tree(const void *q, const void *k, const void *v, const void *seqlens,
+                               int64_t L_max, const void *parent, int B, int N, int Hq, int Hkv,
+                               int D, float scale, const void *o) {
+    if (B < 1 || N < 1 || L_max < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1 ||
+        !isfinite(scale))
+        return QSA_ERR_INVALID_ARG;
+    if (!q || !k || !v || !seqlens || !parent || !o) return QSA_ERR_INVALID_ARG;
+    if (!supported_attn(Hq, Hkv, D) || N > qsa::tree_max_drafts() ||
+        (int64_t)B * N > INT32_MAX / 32 || L_max > INT32_MAX)
+        return QSA_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o))
+        return QSA_ERR_INVALID_ARG;
+    return QSA_OK;
+}
+
+size_t qsa_dense_tree_decode_workspace_size(int B, int N, int Hq, int Hkv, int D) {
+    if (B < 1 || N < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1) return SIZE_MAX;
+    return qsa::tree_ws_bytes(B, N, Hq, D);
+}
+
+qsa_status_t qsa_dense_tree_decode(const qsa_bf16_t *q, const qsa_bf16_t *k_cache,
+                                   const qsa_bf16_t *v_cache, const int32_t *seqlens,
+                                   int64_t L_max, const int32_t *parent, const int32_t *n_draft,
+                                   int B, int N, int Hq, int Hkv, int D, float scale,
+                                   qsa_bf16_t *o, float *lse, void *ws, size_t ws_bytes,
+                                   void *stream) {
+    qsa_status_t st = check_tree(q, k_cache, v_cache, seqlens, L_max, parent, B, N, Hq, Hkv, D,
+                                 scale, o);
+    if (st != QSA_OK) return st;
+    if (!ws || ws_bytes < qsa::tree_ws_bytes(B, N, Hq, D) || !aligned16(ws))
+        return QSA_ERR_WORKSPACE;
+    int sms = 0;
+    st = current_device(&sms);
+    if (st != QSA_OK) return st;
+    return from_cuda(qsa::launch_tree_decode(q, k_cache, v_cache, seqlens, n_draft, L_max,
+                                             nullptr, 0, 0, 0, parent, B, N, Hq, Hkv, D, scale,
+                                             o, lse, ws, static_cast<cudaStream_t>(stream)));
+}
+
+size_t qsa_sparse_tree_decode_workspace_size(int B, int N, int Hq, int D, int r, int budget) {
+    if (B < 1 || N < 1 || Hq < 1 || D < 1 || r < 1 || budget < r || budget % r != 0)
+        return SIZE_MAX;
+    return qsa::tree_ws_bytes(B, N, Hq, D);
+}
+
+qsa_status_t qsa_sparse_tree_decode(const qsa_bf16_t *q, const qsa_bf16_t *k_cache,
+                                    const qsa_bf16_t *v_cache, const int32_t *seqlens,
+                                    int64_t L_max, const int32_t *sel, int64_t sel_batch_stride,
+                                    int64_t sel_row_stride, const int32_t *parent,
+                                    const int32_t *n_draft, int B, int N, int Hq, int Hkv, int D,
+                                    int r, int budget, float scale, qsa_bf16_t *o, float *lse,
+                                    void *ws, size_t ws_bytes, void *stream) {
+    if (r < 1 || budget < r || budget % r != 0 || sel_batch_stride < 0 || sel_row_stride < 0)
+        return QSA_ERR_INVALID_ARG;
+    qsa_status_t st = check_tree(q, k_cache, v_cache, seqlens, L_max, parent, B, N, Hq, Hkv, D,
+                                 scale, o);
+    if (st != QSA_OK) return st;
+    if (!sel) return QSA_ERR_INVALID_ARG;
+    if (r != 4 || budget / r > 1024) return QSA_ERR_UNSUPPORTED_SHAPE;
+    if (!ws || ws_bytes < qsa::tree_ws_bytes(B, N, Hq, D) || !aligned16(ws))
+        return QSA_ERR_WORKSPACE;
+    int sms = 0;
+    st = current_device(&sms);
+    if (st != QSA_OK) return st;
+    return from_cuda(qsa::launch_tree_decode(q, k_cache, v_cache, seqlens, n_draft, L_max, sel,
+                                             sel_batch_stride, sel_row_stride, budget / r,
+                                             parent, B, N, Hq, Hkv, D, scale, o, lse, ws,
+                                             static_cast<cudaStream_t>(stream)));
 }
 
 // ---------------------------------------------------------------- status --

@@ -117,4 +117,36 @@ cudaError_t launch_dense_prefill(const uint16_t *q, const uint16_t *k, const uin
                                  int64_t T, int Hq, int Hkv, int D, float scale, uint16_t *o,
                                  float *lse, cudaStream_t s);
 
+// Rotary positions; per-head norms with the rotation, into outputs or caches, and
+// their backward (rope.cu).  Strides are elements between tokens.
+cudaError_t launch_rope(const void *x, int64_t xs, void *y, int64_t ys, bool fp32, int B,
+                        int64_t T, int H, int D, const double *freq, int rot, bool half,
+                        float mscale, bool transpose, const int64_t *pos, const int64_t *pos0,
+                        int num_sms, cudaStream_t s);
+cudaError_t launch_norm_rope(const uint16_t *q, int64_t qs, const uint16_t *k, int64_t ks,
+                             const uint16_t *v, int64_t vs, int B, int64_t T, int Hq, int Hkv,
+                             int D, const float *qw, const float *kw, float eps,
+                             const double *freq, int rot, bool half, float mscale,
+                             const int64_t *pos, const int64_t *pos0, uint16_t *qo, uint16_t *ko,
+                             uint16_t *vo, const int64_t *slot, int64_t L, void *status,
+                             int num_sms, cudaStream_t s);
+size_t norm_rope_grad_ws_bytes(int64_t n_tok, int Hq, int Hkv, int D);
+cudaError_t launch_norm_rope_grad(const void *d_q, const void *d_k, bool d_fp32,
+                                  const uint16_t *q, int64_t qs, const uint16_t *k, int64_t ks,
+                                  int B, int64_t T, int Hq, int Hkv, int D, const float *qw,
+                                  const float *kw, float eps, const double *freq, int rot,
+                                  bool half, float mscale, const int64_t *pos,
+                                  const int64_t *pos0, void *dq, void *dk, bool dx_fp32,
+                                  float *dqw, float *dkw, void *ws, int num_sms,
+                                  cudaStream_t s);
+
+// Attention for a tree of drafted tokens (tree_attn.cu); sel == nullptr: dense.
+int tree_max_drafts();
+size_t tree_ws_bytes(int B, int N, int Hq, int D);
+cudaError_t launch_tree_decode(const uint16_t *q, const uint16_t *k, const uint16_t *v,
+                               const int32_t *seqlens, const int32_t *n_draft, int64_t L_max,
+                               const int32_t *sel, int64_t sel_b, int64_t sel_n, int kb,
+                               const int32_t *parent, int B, int N, int Hq, int Hkv, int D,
+                               float scale, uint16_t *o, float *lse, void *ws, cudaStream_t s);
+
 }  // namespace qsa

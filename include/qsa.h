@@ -6,7 +6,9 @@
  * GQA attention on the same tensors (the speed-up baseline).  For training,
  * the first stage's indexer distillation loss and gradients and the second
  * stage's sparse attention backward; and the gated delta rule of the
- * hybrid's Gated DeltaNet layers (prefill and decode).
+ * hybrid's Gated DeltaNet layers (prefill and decode).  Around the layer:
+ * rotary positions, per-head norms of queries and keys with the rotation (into
+ * the caches; backward), and attention for a tree of drafted tokens.
  *
  * Sources (web pages about the Qwen3.8-Flash-Next architecture):
  *   [ART]  "用125亿分之6的参数，打平3970亿的旗舰模型", section
@@ -66,6 +68,22 @@ typedef enum {
 } qsa_status_t;
 
 typedef uint16_t qsa_bf16_t; /* raw bf16 bit pattern */
+
+typedef enum { QSA_BF16 = 0, QSA_F32 = 1 } qsa_dtype_t;
+
+/* Which dims of a head form rotary pair i < rot / 2. */
+typedef enum {
+    QSA_ROPE_HALF = 0,       /* i and i + rot / 2 */
+    QSA_ROPE_INTERLEAVED = 1 /* 2 i and 2 i + 1 */
+} qsa_rope_layout_t;
+
+/* How rotary frequencies are stretched for contexts longer than trained. */
+typedef enum {
+    QSA_ROPE_PLAIN = 0,
+    QSA_ROPE_LINEAR = 1,  /* every position divided by the factor */
+    QSA_ROPE_NTK = 2,     /* the base raised, so that the slowest pair is */
+    QSA_ROPE_BY_PARTS = 3 /* slow pairs divided, fast ones kept, a ramp between */
+} qsa_rope_scaling_t;
 
 /*
  * Micro-block mean pooling [ART: consecutive tokens packed into a micro-block
@@ -397,6 +415,142 @@ QSA_API qsa_status_t qsa_gdn_decode(const qsa_bf16_t *q, const qsa_bf16_t *k,
                                     const qsa_bf16_t *v, const float *alpha, const float *beta,
                                     float *state, int B, int H, int dk, int dv, float *o,
                                     void *stream);
+
+/*
+ * Rotary frequencies (host arithmetic only; no device is touched): freq[i],
+ * i < rot / 2, radians per position, in fp64, to be copied to the device once.
+ *   QSA_ROPE_PLAIN     f_i = base^(-2i/rot)
+ *   QSA_ROPE_LINEAR    f_i / factor
+ *   QSA_ROPE_NTK       (base factor^(rot/(rot-2)))^(-2i/rot)   (rot >= 4)
+ *   QSA_ROPE_BY_PARTS  f_i ((1 - w_i) + w_i / factor), w_i = clamp((i - lo) /
+ *                      max(hi - lo, 0.001), 0, 1) with t(beta) = rot ln(orig_len /
+ *                      (2 pi beta)) / (2 ln base), the pair that makes beta turns over
+ *                      orig_len, lo = max(floor(t(beta_fast)), 0) and
+ *                      hi = min(ceil(t(beta_slow)), rot - 1)
+ * *mscale (may be NULL) is the factor on rotated dims: 0.1 ln(factor) + 1 for
+ * QSA_ROPE_BY_PARTS, else 1.  Requires rot even and > 0, base > 1, factor >= 1 and,
+ * by parts, orig_len > 0 and beta_fast >= beta_slow > 0.
+ */
+QSA_API qsa_status_t qsa_rope_frequencies(double base, int rot, int scaling, double factor,
+                                          double orig_len, double beta_fast, double beta_slow,
+                                          double *freq, float *mscale);
+
+/*
+ * Rotary positions.  The first `rot` dims of every head turn in pairs (a, b) by
+ * p * freq[i] at position p, the rest are copied:
+ *     (a, b) -> mscale (a cos - b sin, b cos + a sin)
+ * and with `transpose` the transposed map, (a, b) -> mscale (a cos + b sin,
+ * b cos - a sin): the gradient of the first, and its inverse at mscale 1.
+ * Angles are formed in fp64 and reduced before the fp32 sine and cosine.
+ *   x, y   [B, T, H, D] of `dtype` (qsa_dtype_t); token t of sequence b starts
+ *          (b * T + t) * x_stride (y_stride) elements in, heads packed: H * D <=
+ *          stride, a multiple of 16 bytes.  y may be x with the same stride.
+ *   freq   [rot / 2] fp64 device array
+ *   pos    [B, T] int64 device array, or NULL: p = pos0[b] + t, with pos0 [B] int64
+ *          or NULL (zeros)
+ * D in {32, 64, 128, 256}; rot a multiple of 8, 0 <= rot <= D.  T == 0 is a no-op.
+ */
+QSA_API qsa_status_t qsa_rope(const void *x, int64_t x_stride, void *y, int64_t y_stride,
+                              int dtype, int B, int64_t T, int H, int D, const double *freq,
+                              int rot, int layout, float mscale, int transpose,
+                              const int64_t *pos, const int64_t *pos0, void *stream);
+
+/*
+ * Norms of queries and keys for each head and the rotation in one pass, written to
+ * plain outputs or into the caches (prefill, decode and drafted tokens alike):
+ *     z = x * weight / sqrt(mean(x^2) + eps)   per head of D dims,
+ *     q_out = rope(z_q),  k_out = rope(z_k),  v_out = v
+ * with rope as in qsa_rope; a NULL weight leaves that tensor's norm out.  One
+ * rounding to bf16, at the end.
+ *   q [B, T, Hq, D], k, v [B, T, Hkv, D] bf16 with their strides in elements between
+ *          tokens (so they may be parts of one packed projection); v may be NULL
+ *   q_weight, k_weight [D] fp32 or NULL
+ *   q_out  [B, T, Hq, D] bf16
+ *   k_out, v_out [B, L_max, Hkv, D] bf16 (v_out NULL exactly when v is)
+ *   slot   [B, T] int64 device array of cache rows, distinct within a sequence; a
+ *          negative one leaves both caches as they are; one >= L_max does too and
+ *          is recorded as QSA_ERR_DEVICE.  NULL: row t, and L_max must be T.
+ *   ws     NULL, or a workspace whose first 256 bytes take the status word
+ * q_out may be q (k_out k, v_out v) where the layouts agree.  D, rot and positions
+ * as in qsa_rope.  T == 0 is a no-op.
+ */
+QSA_API qsa_status_t qsa_qk_norm_rope(
+    const qsa_bf16_t *q, int64_t q_stride, const qsa_bf16_t *k, int64_t k_stride,
+    const qsa_bf16_t *v, int64_t v_stride, int B, int64_t T, int Hq, int Hkv, int D,
+    const float *q_weight, const float *k_weight, float eps, const double *freq, int rot,
+    int layout, float mscale, const int64_t *pos, const int64_t *pos0, qsa_bf16_t *q_out,
+    qsa_bf16_t *k_out, qsa_bf16_t *v_out, const int64_t *slot, int64_t L_max, void *ws,
+    void *stream);
+
+/*
+ * Backward of qsa_qk_norm_rope for gradients d_q [B, T, Hq, D] and d_k
+ * [B, T, Hkv, D] of its q_out and k_out, from its inputs q and k (the norms are
+ * computed again).  With r = 1 / sqrt(mean(x^2) + eps), dz the transposed rotation of
+ * the gradient and u = weight dz:
+ *     dx = r (u - x r mean(u x r)),   dweight = sum over tokens and heads of dz x r
+ * and dx = dz where the weight is NULL.  Sums in fp32, in a fixed order: the same
+ * bits on every run of one device.
+ *   d_dtype   type of d_q and d_k, dx_dtype of dq and dk (qsa_dtype_t)
+ *   dq, dk    [B, T, Hq, D], [B, T, Hkv, D]; may be d_q, d_k where the types agree
+ *   dq_weight, dk_weight [D] fp32 or NULL (overwritten; must be NULL without that
+ *             weight); zeros for T == 0
+ *   ws        at least qsa_qk_norm_rope_backward_workspace_size bytes; may be NULL
+ *             when neither weight gradient is wanted
+ */
+QSA_API size_t qsa_qk_norm_rope_backward_workspace_size(int B, int64_t T, int Hq, int Hkv,
+                                                        int D);
+QSA_API qsa_status_t qsa_qk_norm_rope_backward(
+    const void *d_q, const void *d_k, int d_dtype, const qsa_bf16_t *q, int64_t q_stride,
+    const qsa_bf16_t *k, int64_t k_stride, int B, int64_t T, int Hq, int Hkv, int D,
+    const float *q_weight, const float *k_weight, float eps, const double *freq, int rot,
+    int layout, float mscale, const int64_t *pos, const int64_t *pos0, void *dq, void *dk,
+    int dx_dtype, float *dq_weight, float *dk_weight, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Decode attention for a tree of drafted tokens: several drafts of each sequence are
+ * verified in one step.  seqlens[b] tokens of sequence b are in the caches, the last
+ * n = n_draft[b] of them drafts, draft i in row P + i, P = seqlens[b] - n, whatever
+ * its depth (its rotary position, P + depth, is the caller's).  Row i attends to
+ *     S(i) = { u < P } and the chain { P + i, P + parent[i], P + parent[parent[i]], ... }
+ * up to a parent of -1, the last committed token:
+ *     o[b, i, h] = sum_{u in S(i)} softmax_u(scale * q[b, i, h] . k[b, u, g]) v[b, u, g]
+ *     lse[b, i, h] = ln sum_{u in S(i)} exp(scale * q[b, i, h] . k[b, u, g])
+ * Cache rows outside S(i), other branches' among them, may hold anything.
+ *   q [B, N, Hq, D] bf16; k_cache, v_cache [B, L_max, Hkv, D] bf16;
+ *   seqlens [B] int32; n_draft [B] int32 or NULL (N drafts each); parent [B, N] int32
+ *   with -1 <= parent[i] < i; o [B, N, Hq, D] bf16; lse [B, N, Hq] fp32 or NULL.
+ * Rows i >= n of o and lse are left as they were.  Lengths outside 0 <= n <= N,
+ * n <= seqlens[b] <= L_max make every row of the sequence empty (o = 0, lse = -inf),
+ * a parent out of range ends its chain; both are recorded as QSA_ERR_DEVICE.
+ * 1 <= N <= 256; the attention shapes of qsa_dense_gqa_decode.
+ */
+QSA_API size_t qsa_dense_tree_decode_workspace_size(int B, int N, int Hq, int Hkv, int D);
+QSA_API qsa_status_t qsa_dense_tree_decode(const qsa_bf16_t *q, const qsa_bf16_t *k_cache,
+                                           const qsa_bf16_t *v_cache, const int32_t *seqlens,
+                                           int64_t L_max, const int32_t *parent,
+                                           const int32_t *n_draft, int B, int N, int Hq,
+                                           int Hkv, int D, float scale, qsa_bf16_t *o,
+                                           float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * The same over selected micro-blocks: row i's prefix is
+ *     { r*j + k : j in sel[b, i, :], 0 <= j < floor(P / r), 0 <= k < r }
+ * and the tokens after the last complete block, r * floor(P / r) <= u < P; entries
+ * outside [0, floor(P / r)) are ignored, the others must be distinct.  A selection
+ * made by qsa_index_topk_decode with seqlens = P + 1 fits as it is (its own block is
+ * the tail).
+ *   sel    int32, row (b, i) of budget / r entries at sel + b * sel_batch_stride +
+ *          i * sel_row_stride (elements; a row stride of 0 shares one selection)
+ * Constraints besides: r = 4, budget / r <= 1024.
+ */
+QSA_API size_t qsa_sparse_tree_decode_workspace_size(int B, int N, int Hq, int D, int r,
+                                                     int budget);
+QSA_API qsa_status_t qsa_sparse_tree_decode(
+    const qsa_bf16_t *q, const qsa_bf16_t *k_cache, const qsa_bf16_t *v_cache,
+    const int32_t *seqlens, int64_t L_max, const int32_t *sel, int64_t sel_batch_stride,
+    int64_t sel_row_stride, const int32_t *parent, const int32_t *n_draft, int B, int N, int Hq,
+    int Hkv, int D, int r, int budget, float scale, qsa_bf16_t *o, float *lse, void *ws,
+    size_t ws_bytes, void *stream);
 
 /*
  * Measurement aid, not part of the attention path: reads the first `bytes` of
