@@ -92,4 +92,20 @@ bool tensor_map_2d_bf16(CUtensorMap *out, const void *base, uint64_t rows, uint3
     return true;
 }
 
+// A cache [B, rows, cols] bf16 in boxes of 64 columns (128-byte swizzle) x box_rows rows;
+// rows from `rows` on read as zeros.  Encoded on every call: a user's caches come and go.
+bool tensor_map_cache_bf16(CUtensorMap *out, const void *base, uint64_t B, uint64_t rows,
+                           uint32_t cols, uint32_t box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {cols, rows, B};
+    const cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)cols * 2 * rows};
+    const cuuint32_t box[3] = {64, box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
+              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace qsa

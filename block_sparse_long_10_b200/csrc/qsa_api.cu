@@ -628,7 +628,7 @@ static qsa_status_t check_tree(const void *q, const void *k, const void *v, cons
 
 size_t qsa_dense_tree_decode_workspace_size(int B, int N, int Hq, int Hkv, int D) {
     if (B < 1 || N < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1) return SIZE_MAX;
-    return qsa::tree_ws_bytes(B, N, Hq, D);
+    return qsa::tree_dense_ws_bytes(B, N, Hq, Hkv, D);
 }
 
 qsa_status_t qsa_dense_tree_decode(const qsa_bf16_t *q, const qsa_bf16_t *k_cache,
@@ -640,20 +640,20 @@ qsa_status_t qsa_dense_tree_decode(const qsa_bf16_t *q, const qsa_bf16_t *k_cach
     qsa_status_t st = check_tree(q, k_cache, v_cache, seqlens, L_max, parent, B, N, Hq, Hkv, D,
                                  scale, o);
     if (st != QSA_OK) return st;
-    if (!ws || ws_bytes < qsa::tree_ws_bytes(B, N, Hq, D) || !aligned16(ws))
+    if (!ws || ws_bytes < qsa::tree_dense_ws_bytes(B, N, Hq, Hkv, D) || !aligned16(ws))
         return QSA_ERR_WORKSPACE;
     int sms = 0;
     st = current_device(&sms);
     if (st != QSA_OK) return st;
     return from_cuda(qsa::launch_tree_decode(q, k_cache, v_cache, seqlens, n_draft, L_max,
                                              nullptr, 0, 0, 0, parent, B, N, Hq, Hkv, D, scale,
-                                             o, lse, ws, static_cast<cudaStream_t>(stream)));
+                                             o, lse, ws, sms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t qsa_sparse_tree_decode_workspace_size(int B, int N, int Hq, int D, int r, int budget) {
     if (B < 1 || N < 1 || Hq < 1 || D < 1 || r < 1 || budget < r || budget % r != 0)
         return SIZE_MAX;
-    return qsa::tree_ws_bytes(B, N, Hq, D);
+    return qsa::tree_sparse_ws_bytes(B, N, Hq, D, budget / r);
 }
 
 qsa_status_t qsa_sparse_tree_decode(const qsa_bf16_t *q, const qsa_bf16_t *k_cache,
@@ -670,14 +670,14 @@ qsa_status_t qsa_sparse_tree_decode(const qsa_bf16_t *q, const qsa_bf16_t *k_cac
     if (st != QSA_OK) return st;
     if (!sel) return QSA_ERR_INVALID_ARG;
     if (r != 4 || budget / r > 1024) return QSA_ERR_UNSUPPORTED_SHAPE;
-    if (!ws || ws_bytes < qsa::tree_ws_bytes(B, N, Hq, D) || !aligned16(ws))
+    if (!ws || ws_bytes < qsa::tree_sparse_ws_bytes(B, N, Hq, D, budget / r) || !aligned16(ws))
         return QSA_ERR_WORKSPACE;
     int sms = 0;
     st = current_device(&sms);
     if (st != QSA_OK) return st;
     return from_cuda(qsa::launch_tree_decode(q, k_cache, v_cache, seqlens, n_draft, L_max, sel,
                                              sel_batch_stride, sel_row_stride, budget / r,
-                                             parent, B, N, Hq, Hkv, D, scale, o, lse, ws,
+                                             parent, B, N, Hq, Hkv, D, scale, o, lse, ws, sms,
                                              static_cast<cudaStream_t>(stream)));
 }
 

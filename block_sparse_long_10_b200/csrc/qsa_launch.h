@@ -32,6 +32,8 @@ cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, dim3 block, size
 }
 bool tensor_map_2d_bf16(CUtensorMap_st *out, const void *base, uint64_t rows, uint32_t cols,
                         uint32_t box_rows);
+bool tensor_map_cache_bf16(CUtensorMap_st *out, const void *base, uint64_t B, uint64_t rows,
+                           uint32_t cols, uint32_t box_rows);
 
 cudaError_t launch_pool(const uint16_t *k_idx, int B, int64_t T, int Di, int64_t j0,
                         int64_t j1, uint16_t *kp, cudaStream_t s, int num_sms);
@@ -140,13 +142,29 @@ cudaError_t launch_norm_rope_grad(const void *d_q, const void *d_k, bool d_fp32,
                                   float *dqw, float *dkw, void *ws, int num_sms,
                                   cudaStream_t s);
 
-// Attention for a tree of drafted tokens (tree_attn.cu); sel == nullptr: dense.
+// Attention for a tree of drafted tokens (tree_attn.cu): the prefix parts, here over
+// selected blocks (sparse_attn.cu), and what merges them with the drafts' chains.
+// Part x of a (row, head): O at o[x * D], (max, sum) at ml[x * 2], in base 2.
+struct TreePrefix {
+    const int32_t *seqlens, *n_draft;  // [B]; n_draft may be nullptr
+    int N;
+    const int32_t *sel;                // row (b, i) at b * sel_b + i * sel_n
+    int64_t sel_b, sel_n;
+    float *o, *ml;                     // part (row * nsplit + split) * Hq + h
+};
+int tree_sparse_splits(int64_t rows, int kb, int Hkv);
+cudaError_t launch_tree_sparse_prefix(const uint16_t *q, const uint16_t *k, const uint16_t *v,
+                                      const TreePrefix &t, int64_t L_max, int kb, int nsplit,
+                                      int B, int Hq, int Hkv, int D, float scale, int num_sms,
+                                      cudaStream_t s);
 int tree_max_drafts();
-size_t tree_ws_bytes(int B, int N, int Hq, int D);
+size_t tree_dense_ws_bytes(int B, int N, int Hq, int Hkv, int D);
+size_t tree_sparse_ws_bytes(int B, int N, int Hq, int D, int kb);
 cudaError_t launch_tree_decode(const uint16_t *q, const uint16_t *k, const uint16_t *v,
                                const int32_t *seqlens, const int32_t *n_draft, int64_t L_max,
                                const int32_t *sel, int64_t sel_b, int64_t sel_n, int kb,
                                const int32_t *parent, int B, int N, int Hq, int Hkv, int D,
-                               float scale, uint16_t *o, float *lse, void *ws, cudaStream_t s);
+                               float scale, uint16_t *o, float *lse, void *ws, int num_sms,
+                               cudaStream_t s);
 
 }  // namespace qsa

@@ -32,15 +32,18 @@ constexpr int THREADS = WARPS * 32;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
-enum Mode { PREFILL = 0, SPLIT = 1 };
+// TREE: a slice of one drafted token's selection over its committed prefix; entry
+// kb - 1 stands for the tokens after the last complete block.
+enum Mode { PREFILL = 0, SPLIT = 1, TREE = 2 };
 
 // Prefill: 2-stage ring, 3 CTAs per SM (12 warps: the gather is latency-bound
 // and more resident warps beat a deeper ring).  Split decode: 3-stage ring,
-// 2 CTAs per SM (few items per SM, a deeper ring per item pays).
+// 2 CTAs per SM (few items per SM, a deeper ring per item pays).  Trees run like
+// prefill: their rows are many short items that share blocks in L2.
 template <int MODE>
 struct Ring {
-    static constexpr int STAGES = MODE == PREFILL ? 2 : 3;
-    static constexpr int CTAS = MODE == PREFILL ? 3 : 2;
+    static constexpr int STAGES = MODE == SPLIT ? 3 : 2;
+    static constexpr int CTAS = MODE == SPLIT ? 2 : 3;
 };
 
 template <int D, int HKV, int STAGES>
@@ -53,7 +56,7 @@ struct Cfg {
     static constexpr int STAGE_K = KS * ROW;
     static constexpr int STAGE_BYTES = 2 * STAGE_K;   // K then V
     static constexpr int OFF_SEL = STAGES * STAGE_BYTES;
-    static constexpr int MAX_ENT = 1024;
+    static constexpr int MAX_ENT = 1028;  // TREE: 1024 and the tail
     static constexpr int BYTES = OFF_SEL + MAX_ENT * 4;
     // merge area (aliases the stage ring once it has drained)
     static constexpr int MERGE_BYTES = WARPS * (D * 8 + 16) * 4;
@@ -78,6 +81,7 @@ struct Args {
     float *part;             // split mode: [B, nsplit, Hq, D + 2]
     void *status;            // workspace (status word) or nullptr
     int64_t total_items;
+    TreePrefix tree;         // TREE mode
 };
 
 template <int D, int G, int HKV, int MODE>
@@ -106,6 +110,19 @@ __global__ void __launch_bounds__(THREADS, Ring<MODE>::CTAS) sparse_attn_kernel(
             e0 = 0;
             e1 = a.kb;
             qrow = a.q + row * Hq * D;
+        } else if (MODE == TREE) {
+            row = item / a.nsplit;
+            b = row / a.tree.N;
+            const int i = (int)(row - b * a.tree.N);
+            const int split = (int)(item - row * a.nsplit);
+            const int64_t S = a.seqlens[b];
+            const int n = a.tree.n_draft ? a.tree.n_draft[b] : a.tree.N;
+            // no such draft, or lengths that the merge reports
+            if (i >= n || n > a.tree.N || S < n || S > a.Tk) continue;
+            p = S - n - 1;
+            e0 = split * a.chunk;
+            e1 = min(e0 + a.chunk, a.kb);
+            qrow = a.q + row * Hq * D;
         } else {
             b = item / a.nsplit;
             row = b;
@@ -116,7 +133,7 @@ __global__ void __launch_bounds__(THREADS, Ring<MODE>::CTAS) sparse_attn_kernel(
             if (e1 > a.kb) e1 = a.kb;
             qrow = a.q + b * Hq * D;
         }
-        if (p >= a.Tk || p < 0) {
+        if (MODE != TREE && (p >= a.Tk || p < 0)) {
             if (tid == 0) record_status(a.status, QSA_ERR_DEVICE);
             p = -1;  // empty token set
         }
@@ -124,6 +141,17 @@ __global__ void __launch_bounds__(THREADS, Ring<MODE>::CTAS) sparse_attn_kernel(
         const uint16_t *kb_ = a.k + b * a.Tk * HKV * D;
         const uint16_t *vb_ = a.v + b * a.Tk * HKV * D;
         for (int i = tid; i < n_ent; i += THREADS) {
+            if (MODE == TREE) {
+                const int64_t whole = (p + 1) / 4;
+                const int e = e0 + i;
+                int j = (int)whole;
+                if (e < a.kb - 1) {
+                    j = a.tree.sel[b * a.tree.sel_b + (row - b * a.tree.N) * a.tree.sel_n + e];
+                    if (j >= whole) j = -1;
+                }
+                s_blk[i] = j;
+                continue;
+            }
             int j = a.sel ? a.sel[row * a.kb + e0 + i] : e0 + i;
             if (j < 0 || (int64_t)j * 4 > p) j = -1;
             s_blk[i] = j;
@@ -298,6 +326,13 @@ __global__ void __launch_bounds__(THREADS, Ring<MODE>::CTAS) sparse_attn_kernel(
                 a.o[(row * Hq + h) * D + d] = to_bf16_bits(L > 0.f ? O / L : 0.f);
                 if (a.lse && d == 0)
                     a.lse[row * Hq + h] = L > 0.f ? (M + __log2f(L)) * LN2 : -INFINITY;
+            } else if (MODE == TREE) {
+                const int64_t x = item * Hq + h;
+                a.tree.o[x * D + d] = O;
+                if (d == 0) {
+                    a.tree.ml[x * 2] = M;
+                    a.tree.ml[x * 2 + 1] = L;
+                }
             } else {
                 float *pp = a.part + ((item * Hq) + h) * (D + 2);
                 pp[d] = O;
@@ -405,6 +440,29 @@ cudaError_t launch_split_decode(const uint16_t *q, const uint16_t *k, const uint
                                 (const float *)part, B, Hq, nsplit, o, lse);
     return launch_dependent(sat::split_combine_kernel<128>, cgrid, dim3(256), 0, s,
                             (const float *)part, B, Hq, nsplit, o, lse);
+}
+
+// A tree's rows fill the GPU three times over, or each is split until they do; a slice
+// keeps at least two stages.
+int tree_sparse_splits(int64_t rows, int kb, int Hkv) {
+    const int64_t most = (kb + 1) / (2 * sparse_attn_blocks_per_stage(Hkv));
+    int64_t ns = 148 * sat::Ring<sat::TREE>::CTAS / rows;
+    if (ns > most) ns = most;
+    return (int)(ns < 1 ? 1 : ns);
+}
+
+cudaError_t launch_tree_sparse_prefix(const uint16_t *q, const uint16_t *k, const uint16_t *v,
+                                      const TreePrefix &t, int64_t L_max, int kb, int nsplit,
+                                      int B, int Hq, int Hkv, int D, float scale, int num_sms,
+                                      cudaStream_t s) {
+    sat::Args a{};
+    a.q = q; a.k = k; a.v = v; a.seqlens = t.seqlens; a.B = B; a.Tk = L_max; a.Hq = Hq;
+    a.kb = kb + 1; a.nsplit = nsplit; a.chunk = (kb + nsplit) / nsplit;
+    a.scale_log2 = scale * sat::LOG2E; a.tree = t;
+    a.total_items = (int64_t)B * t.N * nsplit;
+    const int64_t slots = (int64_t)num_sms * sat::Ring<sat::TREE>::CTAS;
+    const int64_t grid = a.total_items < slots ? a.total_items : slots;
+    return sat::dispatch<sat::TREE>(a, D, Hq / Hkv, Hkv, (int)grid, s);
 }
 
 }  // namespace qsa

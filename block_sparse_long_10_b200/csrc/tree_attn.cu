@@ -7,13 +7,16 @@
 // blocks and the unpooled tail (sparse), and to its own chain i, parent[i],
 // parent[parent[i]], ...: softmax over both parts together.
 //
-// The two parts are kept apart.  The prefix has no mask that differs between rows.
-// The chain is a handful of tokens with a mask of its own per row: it is walked
-// token by token in fp32, so what a masked draft's cache rows hold (infinities,
-// NaN) never enters another branch, as a zero times it in a matrix product would.
-// Both parts leave (max, sum, O) and meet in tree_merge_kernel.
+// The two parts are kept apart.  The dense prefix has no mask that differs between
+// rows: it is two matrix products (tree_dense_kernel).  Selections differ from row to
+// row: they are gathered row by row (sparse_attn.cu).  The chain is a handful of
+// tokens with a mask of its own per row: it is walked token by token in fp32, so what a
+// masked draft's cache rows hold (infinities, NaN) never enters another branch, as a
+// zero times it in a matrix product would.  Both parts leave (max, sum, O) in base 2
+// and meet in tree_merge_kernel.
 #include "qsa_common.cuh"
 #include "qsa_launch.h"
+#include "sm100.cuh"
 
 namespace qsa {
 
@@ -43,8 +46,455 @@ struct Lens {
     }
 };
 
-// One query head against single tokens: 4 groups of 8 lanes take a token each; a
-// lane holds E = D / 8 dims.  Running (max, sum, O) per group, in base 2.
+struct Args {
+    const uint16_t *q;   // [B, N, Hq, D]
+    const uint16_t *k;   // [B, L_max, Hkv, D]
+    const uint16_t *v;
+    Lens lens;
+    const int32_t *parent;  // [B, N]
+    int B, N, Hq, Hkv, G;
+    float scale_log2;
+    // prefix parts: part x holds O[x * D ..] and (max, sum)[x * 2 ..]
+    float *part, *ml;
+    int nsplit;          // sparse: parts (row * nsplit + split) * Hq + h
+    int units, rows;     // dense: units per sequence, rows per unit
+    int32_t *first, *last;  // dense: [B * units] first and last CTA of a unit
+    uint16_t *o;
+    float *lse;
+    void *status;
+};
+
+// ------------------------------------------------------------ dense prefix --
+// Rows of one KV head, (draft, head) pairs r = i * G + h, are cut into units of
+// 128 * NT.  A unit times a run of 128-token tiles of its prefix is a flash attention
+// on the tensor cores: S = Q K^T and O += P V with 128 x 128 x 16 MMAs (tcgen05), S, P
+// and O in TMEM, a thread per row for the softmax.
+//
+// Work split: the units' tiles, in one row over all sequences, are cut into equal runs,
+// one per SM, whatever the lengths (known on the device only).  A run may end one unit
+// and begin another; each such segment leaves one part per row, in slot CTA + unit
+// (every segment raises one of the two).
+//
+// Two softmax streams of 128 threads keep the tensor core busy: with NT = 2 they are
+// two row tiles over the same K and V, with NT = 1 (at most 128 rows) even and odd
+// token tiles of one row tile, merged at the end of the segment.  Step t of a segment is
+// S(t), softmax, O += P V (t); the MMA warp issues S(t + 2) right after P V (t), so one
+// stream's products run under the other's softmax.  P (bf16) overwrites the S it came
+// from.  O is rescaled only when the running maximum has grown by more than 8 (a
+// factor 256) since its last rescale: sums and O stay far inside fp32, and P keeps bf16's
+// relative precision at any size.  P is rounded to bf16 for the matrix product; the sum
+// is taken of the unrounded values, in fp32.
+constexpr int KT = 128;        // tokens per tile
+constexpr int ATOM = KT * 128; // bytes of a 64-column half tile in shared memory
+constexpr int SOFT = 256;      // softmax threads
+constexpr int THREADS = SOFT + 64;
+constexpr float GROWTH = 8.f;
+constexpr int MAX_CTAS = 160;  // what the workspace is sized for
+constexpr uint64_t WAIT_NS = 2000000000ull;
+
+template <int D, int NT>
+struct Cfg {
+    static constexpr int TILE = KT * D * 2;
+    static constexpr int OFF_RING = NT * TILE;
+    static constexpr int ROOM = 227 * 1024 - 1024 - 512;  // alignment; barriers
+    static constexpr int FIT = (ROOM - OFF_RING) / TILE;
+    static constexpr int SLOTS = FIT > 8 ? 8 : FIT;
+    static constexpr int OFF_BAR = OFF_RING + SLOTS * TILE;
+    static constexpr int BYTES = 1024 + OFF_BAR + 512;
+    static_assert((2 * SLOTS + 6) * 8 + 16 <= 512, "barriers");
+    static_assert(NT == 2 || 2 * 128 * 8 <= TILE, "the streams' sums fit in the query tile");
+    // TMEM columns
+    static constexpr int O_COL = 256;
+    static constexpr uint32_t IDESC_S = sm100::idesc_bf16_f32(128, KT);
+    static constexpr uint32_t IDESC_O = sm100::idesc_bf16_f32(128, D) | sm100::IDESC_B_MNMAJOR;
+};
+
+// A run of tiles of one unit.
+struct Seg {
+    int64_t b, t0, P;  // first tile; committed tokens
+    int g, qt, nd, n;  // tiles
+    bool begins, ends; // the unit's first (last) tile is in it
+};
+
+// The segments of this CTA, in order.  Each thread that asks walks by itself.
+template <int NT>
+struct Walk {
+    int64_t pos, hi, b, b0;  // b0: flat index of sequence b's first tile
+
+    QSA_DEVICE static int64_t tiles(const Seq &s) { return (s.P + KT - 1) / KT; }
+    QSA_DEVICE static int units(const Args &a, const Seq &s) {
+        return (s.n * a.G + 128 * NT - 1) / (128 * NT);
+    }
+    QSA_DEVICE static int64_t weight(const Args &a, int64_t b) {
+        const Seq s = a.lens.at(b);
+        return tiles(s) * units(a, s) * a.Hkv;
+    }
+    // Whole warps; false: nothing for this CTA.
+    QSA_DEVICE bool start(const Args &a, int lane) {
+        int64_t total = 0;
+        for (int64_t i = 0; i < a.B; i += 32) total += i + lane < a.B ? weight(a, i + lane) : 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        const int64_t ctas = total < gridDim.x ? total : gridDim.x;
+        if (blockIdx.x >= ctas) return false;
+        pos = total * blockIdx.x / ctas;
+        hi = total * (blockIdx.x + 1) / ctas;
+        b0 = 0;
+        for (int64_t i = 0;; i += 32) {
+            const int64_t w = i + lane < a.B ? weight(a, i + lane) : 0;
+            int64_t end = w;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, end, o);
+                if (lane >= o) end += y;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, b0 + end > pos);
+            if (past) {
+                const int f = __ffs(past) - 1;
+                b = i + f;
+                b0 += __shfl_sync(0xffffffffu, end - w, f);
+                return true;
+            }
+            b0 += __shfl_sync(0xffffffffu, end, 31);
+        }
+    }
+    QSA_DEVICE bool next(const Args &a, Seg &s) {
+        if (pos >= hi) return false;
+        Seq sq = a.lens.at(b);
+        int64_t w = tiles(sq) * units(a, sq) * a.Hkv;
+        while (pos >= b0 + w) {
+            b0 += w;
+            sq = a.lens.at(++b);
+            w = tiles(sq) * units(a, sq) * a.Hkv;
+        }
+        const int64_t nt = tiles(sq), u = (pos - b0) / nt;
+        const int qn = units(a, sq);
+        s.b = b;
+        s.P = sq.P;
+        s.nd = sq.n;
+        s.g = (int)(u / qn);
+        s.qt = (int)(u - (int64_t)s.g * qn);
+        s.t0 = pos - b0 - u * nt;
+        const int64_t n = nt - s.t0 < hi - pos ? nt - s.t0 : hi - pos;
+        s.n = (int)n;
+        s.begins = s.t0 == 0;
+        s.ends = s.t0 + n == nt;
+        pos += n;
+        return true;
+    }
+};
+
+// Order of a segment's 2 n tiles in the ring: K0, then (NT = 1) K(j + 1), V(j) by turns,
+// or (NT = 2) V(j), K(j + 1): the order in which the MMAs want and free them.
+template <int NT>
+QSA_DEVICE uint32_t ring_k(uint32_t base, int j) {
+    return NT == 2 ? base + 2 * j : base + (j == 0 ? 0 : 2 * j - 1);
+}
+template <int NT>
+QSA_DEVICE uint32_t ring_v(uint32_t base, int j, int n) {
+    return NT == 2 ? base + 2 * j + 1 : base + (j == n - 1 ? 2 * j + 1 : 2 * j + 2);
+}
+
+QSA_DEVICE void soft_sync() { asm volatile("bar.sync 1, %0;\n" ::"n"(SOFT) : "memory"); }
+
+template <int D, int NT>
+__global__ void __launch_bounds__(THREADS, 1)
+    tree_dense_kernel(const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const Args a) {
+    using C = Cfg<D, NT>;
+    constexpr int SL = C::SLOTS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR), *empty = full + SL;
+    uint64_t *sfull = empty + SL, *pready = sfull + 2, *odone = pready + 2, *qready = odone + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(qready + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    // the merge kernel may start on the chains
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    Walk<NT> walk;
+    if (!walk.start(a, lane)) return;
+    if (tid == 0) {
+        for (int i = 0; i < SL; ++i) {
+            sm100::mbar_init(&full[i], 1);
+            sm100::mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            sm100::mbar_init(&sfull[i], 1);
+            sm100::mbar_init(&pready[i], 128);
+        }
+        sm100::mbar_init(odone, 1);
+        sm100::mbar_init(qready, SOFT);
+        *abort_flag = 0;
+        sm100::fence_mbar_init();
+    }
+    if (warp == SOFT / 32 + 1) sm100::tmem_alloc(tmem_slot, 512);
+    sm100::tc_fence_before();
+    __syncthreads();
+    sm100::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t ring = smem_u32(sm + C::OFF_RING);
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        return sm100::mbar_wait(bar, parity & 1, abort_flag, WAIT_NS, a.status);
+    };
+    Seg sg;
+
+    if (warp == SOFT / 32) {
+        // ------------------------------------------------------ producer --
+        if (lane == 0) {
+            sm100::prefetch_tensormap(&tm_k);
+            sm100::prefetch_tensormap(&tm_v);
+            uint32_t it = 0;
+            bool dead = false;
+            auto put = [&](const CUtensorMap *m, int64_t tile) {
+                const uint32_t slot = it % SL;
+                if (dead || !wait(&empty[slot], (it / SL) + 1)) {
+                    dead = true;
+                    return;
+                }
+                sm100::mbar_arrive_expect_tx(&full[slot], C::TILE);
+#pragma unroll
+                for (int at = 0; at < D / 64; ++at)
+                    sm100::tma_load_3d(ring + slot * C::TILE + at * ATOM, m, sg.g * D + at * 64,
+                                       (int32_t)(tile * KT), (int32_t)sg.b, &full[slot]);
+                ++it;
+            };
+            while (walk.next(a, sg)) {
+                put(&tm_k, sg.t0);
+                for (int j = 0; j < sg.n; ++j) {
+                    if (NT == 1 && j + 1 < sg.n) put(&tm_k, sg.t0 + j + 1);
+                    put(&tm_v, sg.t0 + j);
+                    if (NT == 2 && j + 1 < sg.n) put(&tm_k, sg.t0 + j + 1);
+                }
+            }
+            // no copy may land after the CTA has gone
+            for (uint32_t i = it > SL ? it - SL : 0; i < it; ++i)
+                sm100::mbar_wait_for(&full[i % SL], (i / SL) & 1, 100000000ull);
+        }
+    } else if (warp == SOFT / 32 + 1) {
+        // ----------------------------------------------------------- MMA --
+        if (lane == 0) {
+            const uint32_t qs = smem_u32(sm);
+            uint32_t base = 0, done[2] = {0, 0}, segs = 0;
+            while (walk.next(a, sg)) {
+                const int steps = NT * sg.n;
+                wait(qready, segs);
+                sm100::tc_fence_after();
+                auto scores = [&](int t) {
+                    const int s = t & 1;
+                    const uint32_t idx = ring_k<NT>(base, NT == 2 ? t >> 1 : t), slot = idx % SL;
+                    if (NT == 1 || s == 0) wait(&full[slot], idx / SL);
+                    const uint32_t qa = qs + (NT == 2 ? s * C::TILE : 0);
+                    const uint32_t ka = ring + slot * C::TILE;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = (k >> 2) * ATOM + (k & 3) * 32;
+                        sm100::mma_bf16(tmem + s * KT, sm100::smem_desc_kmajor(qa + off, 128),
+                                        sm100::smem_desc_kmajor(ka + off, 128), C::IDESC_S, k > 0);
+                    }
+                    sm100::mma_commit(&sfull[s]);
+                    if (NT == 1 || s == 1) sm100::mma_commit(&empty[slot]);
+                };
+                scores(0);
+                if (steps > 1) scores(1);
+                for (int t = 0; t < steps; ++t) {
+                    const int s = t & 1;
+                    const uint32_t idx = ring_v<NT>(base, NT == 2 ? t >> 1 : t, sg.n);
+                    const uint32_t slot = idx % SL;
+                    wait(&pready[s], done[s]++);
+                    if (NT == 1 || s == 0) wait(&full[slot], idx / SL);
+                    sm100::tc_fence_after();
+                    const uint32_t va = ring + slot * C::TILE;
+#pragma unroll
+                    for (int k = 0; k < KT / 16; ++k)
+                        sm100::mma_bf16_ta(tmem + C::O_COL + s * D, tmem + s * KT + k * 8,
+                                           sm100::smem_desc_mnmajor(va + k * 2048, ATOM),
+                                           C::IDESC_O, t > 1 || k > 0);
+                    if (NT == 1 || s == 1) sm100::mma_commit(&empty[slot]);
+                    if (t + 2 < steps) scores(t + 2);
+                }
+                sm100::mma_commit(odone);
+                base += 2 * sg.n;
+                ++segs;
+            }
+        }
+    } else {
+        // ------------------------------------------------------- softmax --
+        const int s = warp >> 2, r = tid & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's quarter of TMEM
+        const uint32_t s_tm = tmem + lanes + s * KT, o_tm = tmem + lanes + C::O_COL + s * D;
+        const float sc = fabsf(a.scale_log2);
+        const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // the sign moves into Q
+        float2 *s_ml = reinterpret_cast<float2 *>(sm);  // [2][128]: the query tile, once done with
+        uint32_t base = 0, got = 0, segs = 0;
+        while (walk.next(a, sg)) {
+            const int steps = NT * sg.n;
+            const int R = sg.nd * a.G, r0 = sg.qt * 128 * NT;
+            if (segs > 0) soft_sync();  // the sums have been read
+            for (int i = tid; i < NT * 128 * (D / 8); i += SOFT) {
+                const int row = i / (D / 8), ch = i % (D / 8);
+                const int rr = r0 + row, d = rr / a.G;
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (rr < R)
+                    x = *reinterpret_cast<const uint4 *>(
+                        a.q + ((sg.b * a.N + d) * a.Hq + sg.g * a.G + (rr - d * a.G)) * D + ch * 8);
+                x.x ^= flip; x.y ^= flip; x.z ^= flip; x.w ^= flip;
+                *reinterpret_cast<uint4 *>(sm + (row >> 7) * C::TILE + (ch >> 3) * ATOM +
+                                           (row & 127) * 128 + (((ch ^ row) & 7) << 4)) = x;
+            }
+            sm100::fence_async_shared();
+            sm100::tc_fence_before();
+            sm100::mbar_arrive(qready);
+            if (tid == 0) {
+                const int64_t u = (sg.b * a.Hkv + sg.g) * a.units + sg.qt;
+                if (sg.begins) a.first[u] = blockIdx.x;
+                if (sg.ends) a.last[u] = blockIdx.x;
+            }
+            const int row = r0 + (NT == 2 ? s * 128 : 0) + r;
+            const bool on = __any_sync(0xffffffffu, row < R);  // a live row in this warp
+            float m = -INFINITY, l = 0.f;
+            for (int t = s; t < steps; t += 2) {
+                const int j = NT == 2 ? t >> 1 : t;
+                const int64_t left = sg.P - (sg.t0 + j) * KT;  // tokens in this tile
+                wait(&sfull[s], got++);
+                sm100::tc_fence_after();
+                if (on) {
+                    uint32_t x[KT];
+                    sm100::tmem_ld128(s_tm, x);
+                    if (left < KT) {
+#pragma unroll
+                        for (int c = 0; c < KT; ++c)
+                            if (c >= left) x[c] = 0xff800000u;  // -inf
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < KT; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(x[c]));
+                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+                    const bool grow = mt > m + GROWTH;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float mn = grow ? mt : m;
+                        const float f = grow ? fast_exp2(m - mn) : 1.f;
+                        l *= f;
+                        m = mn;
+                        if (t > 1) {
+#pragma unroll
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t y[32];
+                                sm100::tmem_ld32(o_tm + c, y);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+                                sm100::tmem_st32(o_tm + c, y);
+                            }
+                        }
+                    }
+                    const float mu = m == -INFINITY ? 0.f : m;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < KT; c += 32) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float p0 = fast_exp2(fmaf(__uint_as_float(x[c + e]), sc, -mu));
+                            float p1 = fast_exp2(fmaf(__uint_as_float(x[c + e + 1]), sc, -mu));
+                            if (left < KT) {  // 0 * -inf at a scale of 0
+                                if (c + e >= left) p0 = 0.f;
+                                if (c + e + 1 >= left) p1 = 0.f;
+                            }
+                            sum[e & 2] += p0;
+                            sum[(e & 2) + 1] += p1;
+                            pk[e / 2] = pack_bf16x2(p0, p1);
+                        }
+                        sm100::tmem_st16(s_tm + c / 2, pk);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    sm100::tmem_wait_st();
+                }
+                if (left < KT && (NT == 1 || s == 0)) {
+                    // rows behind the prefix may hold anything: 0 * V must be 0
+                    const uint32_t idx = ring_v<NT>(base, j, sg.n), slot = idx % SL;
+                    wait(&full[slot], idx / SL);
+                    uint8_t *vt = sm + C::OFF_RING + slot * C::TILE;
+                    const int dead = KT - (int)left;  // rows, 8 chunks in each half tile
+                    for (int i = r; i < dead * (D / 8); i += 128) {
+                        const int at = i / (dead * 8), w = i - at * dead * 8;
+                        *reinterpret_cast<uint4 *>(vt + at * ATOM + (int)left * 128 + w * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    sm100::fence_async_shared();
+                }
+                sm100::tc_fence_before();
+                sm100::mbar_arrive(&pready[s]);
+            }
+            wait(odone, segs);
+            sm100::tc_fence_after();
+            const int64_t unit = (sg.b * a.Hkv + sg.g) * a.units + sg.qt;
+            const int64_t slot_row = (blockIdx.x + unit) * a.rows;
+            if (NT == 2) {
+                if (on) {
+                    float *out = a.part + (slot_row + s * 128 + r) * D;
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t y[32];
+                        sm100::tmem_ld32(o_tm + c, y);
+                        if (row < R)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                *reinterpret_cast<uint4 *>(out + c + e) =
+                                    make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                    }
+                    if (row < R)
+                        *reinterpret_cast<float2 *>(a.ml + (slot_row + s * 128 + r) * 2) =
+                            make_float2(m, l);
+                }
+            } else {
+                // the streams' parts become one; each writes half of the columns
+                s_ml[s * 128 + r] = make_float2(m, l);
+                soft_sync();
+                if (on) {
+                    const float2 w0 = s_ml[r], w1 = s_ml[128 + r];
+                    const float M = fmaxf(w0.x, w1.x), Mu = M == -INFINITY ? 0.f : M;
+                    const float f0 = fast_exp2(w0.x - Mu), f1 = fast_exp2(w1.x - Mu);
+                    float *out = a.part + (slot_row + r) * D;
+#pragma unroll 1
+                    for (int c = s * (D / 2); c < (s + 1) * (D / 2); c += 32) {
+                        uint32_t y[32], z[32];
+                        sm100::tmem_ld32(tmem + lanes + C::O_COL + c, y);
+                        if (steps > 1) {
+                            sm100::tmem_ld32(tmem + lanes + C::O_COL + D + c, z);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) z[e] = 0;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            y[e] = __float_as_uint(__uint_as_float(y[e]) * f0 +
+                                                   __uint_as_float(z[e]) * f1);
+                        if (row < R)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                *reinterpret_cast<uint4 *>(out + c + e) =
+                                    make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                    }
+                    if (row < R && s == 0)
+                        *reinterpret_cast<float2 *>(a.ml + (slot_row + r) * 2) =
+                            make_float2(M, w0.y * f0 + w1.y * f1);
+                }
+            }
+            base += 2 * sg.n;
+            ++segs;
+        }
+    }
+    sm100::tc_fence_before();
+    __syncthreads();
+    sm100::tc_fence_after();
+    if (warp == SOFT / 32 + 1) sm100::tmem_dealloc(tmem, 512);
+}
+
+// --------------------------------------------------------- chains and merge --
+// One query head against single tokens: groups of 8 lanes take a token each; a lane
+// holds E = D / 8 dims.  Running (max, sum, O) per group, in base 2.
 template <int D>
 struct Row {
     static constexpr int E = D / 8;
@@ -83,10 +533,11 @@ struct Row {
     // token with cache rows k and v; `on` false: the group sits out (all lanes call)
     QSA_DEVICE void token(const uint16_t *k, const uint16_t *v, bool on, int li,
                           float scale_log2) {
-        float f[E];
+        float f[E], w[E];
         float x = 0.f;
         if (on) {
             load16(k + li * E, f);
+            load16(v + li * E, w);
 #pragma unroll
             for (int e = 0; e < E; ++e) x += q[e] * f[e];
         }
@@ -94,17 +545,16 @@ struct Row {
         x += __shfl_xor_sync(0xffffffffu, x, 2);
         x += __shfl_xor_sync(0xffffffffu, x, 4);
         if (!on) return;
-        load16(v + li * E, f);
         x *= scale_log2;
         const float mn = fmaxf(m, x);
         const float mu = mn == -INFINITY ? 0.f : mn;
         const float fa = fast_exp2(m - mu), p = fast_exp2(x - mu);
         l = l * fa + p;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * fa + p * f[e];
+        for (int e = 0; e < E; ++e) o[e] = o[e] * fa + p * w[e];
         m = mn;
     }
-    // the four groups' parts become one, in every lane
+    // the warp's four groups' parts become one, in every lane
     QSA_DEVICE void join_groups() {
 #pragma unroll
         for (int x = 8; x < 32; x <<= 1) {
@@ -118,96 +568,30 @@ struct Row {
     }
 };
 
-struct Args {
-    const uint16_t *q;   // [B, N, Hq, D]
-    const uint16_t *k;   // [B, L_max, Hkv, D]
-    const uint16_t *v;
-    Lens lens;
-    const int32_t *parent;  // [B, N]
-    const int32_t *sel;     // selected blocks of row (b, i) at b * sel_b + i * sel_n
-    int64_t sel_b, sel_n;
-    int kb;
-    int N, Hq, Hkv, G, nsplit;
-    float scale_log2;
-    float *part;            // [B * N, nsplit, Hq, D + 2]
-    uint16_t *o;
-    float *lse;
-    void *status;
-};
-
 constexpr int WARPS = 4;
 
-// Prefix part of row (b, i), heads in warps, one slice of its tokens per block.
+// A block per (row, head): its 16 groups of 8 lanes share out the chain's tokens, then
+// (after the prefix kernel) the prefix parts.  Runs of 74 parts (one long sequence over
+// all SMs) and of 1 take the same path; the chain is done under the prefix kernel's tail.
 template <int D, bool SPARSE>
-__global__ void __launch_bounds__(WARPS * 32) tree_prefix_kernel(const Args a) {
-    const int64_t row = blockIdx.x / a.nsplit;
-    const int split = (int)(blockIdx.x - row * a.nsplit);
-    const int64_t b = row / a.N;
-    const int i = (int)(row - b * a.N);
-    const Seq sq = a.lens.at(b);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = lane >> 3, li = lane & 7;
-    const int h = blockIdx.y * WARPS + warp;
-    if (i >= sq.n || h >= a.Hq) return;
-    const int64_t tok = (int64_t)a.Hkv * D;
-    const uint16_t *k = a.k + b * a.lens.L_max * tok + (h / a.G) * D;
-    const uint16_t *v = a.v + b * a.lens.L_max * tok + (h / a.G) * D;
-    Row<D> r;
-    r.start(a.q + (row * a.Hq + h) * D, li);
-    if (SPARSE) {
-        const int64_t whole = sq.P / 4;
-        const int chunk = (a.kb + a.nsplit - 1) / a.nsplit;
-        const int e1 = min((split + 1) * chunk, a.kb);
-        const int32_t *sel = a.sel + b * a.sel_b + i * a.sel_n;
-        for (int e = split * chunk; e < e1; ++e) {
-            const int64_t j = sel[e];
-            const bool on = j >= 0 && j < whole;
-            const int64_t u = on ? j * 4 + grp : 0;
-            r.token(k + u * tok, v + u * tok, on, li, a.scale_log2);
-        }
-        if (split == 0) {
-            const int64_t u = whole * 4 + grp;
-            const bool on = u < sq.P;
-            r.token(k + (on ? u : 0) * tok, v + (on ? u : 0) * tok, on, li, a.scale_log2);
-        }
-    } else {
-        const int64_t chunk = (sq.P + a.nsplit - 1) / a.nsplit;
-        const int64_t u1 = min((split + 1) * chunk, sq.P);
-        for (int64_t u0 = split * chunk; u0 < u1; u0 += 4) {
-            const bool on = u0 + grp < u1;
-            const int64_t u = on ? u0 + grp : 0;
-            r.token(k + u * tok, v + u * tok, on, li, a.scale_log2);
-        }
-    }
-    r.join_groups();
-    float *pp = a.part + ((row * a.nsplit + split) * a.Hq + h) * (D + 2);
-    if (grp == 0) {
-#pragma unroll
-        for (int e = 0; e < Row<D>::E; ++e) pp[li * Row<D>::E + e] = r.o[e];
-        if (li == 0) {
-            pp[D] = r.m;
-            pp[D + 1] = r.l;
-        }
-    }
-}
-
-// Chain part and merge: a warp per (row, head).
-template <int D>
 __global__ void __launch_bounds__(WARPS * 32) tree_merge_kernel(const Args a) {
-    constexpr int E = Row<D>::E;
-    __shared__ int s_par[MAX_N];
+    constexpr int E = Row<D>::E, GROUPS = WARPS * 4;
+    __shared__ int s_par[MAX_N], s_chain[MAX_N];
+    __shared__ int s_len;
+    __shared__ float s_o[WARPS][D], s_m[WARPS], s_l[WARPS];
     const int64_t row = blockIdx.x;
     const int64_t b = row / a.N;
-    const int i = (int)(row - b * a.N);
+    const int i = (int)(row - b * a.N), h = blockIdx.y;
     const Seq sq = a.lens.at(b);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = lane >> 3, li = lane & 7;
-    const int h = blockIdx.y * WARPS + warp;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, li = lane & 7;
+    const int grp = tid >> 3;
     if (sq.bad) {
-        if (i == 0 && blockIdx.y == 0 && threadIdx.x == 0) record_status(a.status, QSA_ERR_DEVICE);
+        if (i == 0 && h == 0 && tid == 0) record_status(a.status, QSA_ERR_DEVICE);
     } else if (i >= sq.n) {
         return;
     }
     // a parent must come before its child; any other value ends the chain
-    for (int j = threadIdx.x; j <= i && j < sq.n; j += WARPS * 32) {
+    for (int j = tid; j <= i && j < sq.n; j += WARPS * 32) {
         int p = a.parent[b * a.N + j];
         if (p < -1 || p >= j) {
             record_status(a.status, QSA_ERR_DEVICE);
@@ -216,86 +600,173 @@ __global__ void __launch_bounds__(WARPS * 32) tree_merge_kernel(const Args a) {
         s_par[j] = p;
     }
     __syncthreads();
-    griddep_wait();  // the prefix parts
-    if (h >= a.Hq) return;
+    if (tid == 0) {
+        int len = 0;
+        if (!sq.bad)
+            for (int j = i; j >= 0; j = s_par[j]) s_chain[len++] = j;
+        s_len = len;
+    }
+    __syncthreads();
     Row<D> r;
     r.start(a.q + (row * a.Hq + h) * D, li);
-    if (!sq.bad) {
-        const int64_t tok = (int64_t)a.Hkv * D;
-        const int64_t base = (b * a.lens.L_max + sq.P) * tok + (h / a.G) * D;
-        for (int j = i; j >= 0;) {
-            int mine = -1;  // four steps of the chain, one a group
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                if (s == grp) mine = j;
-                if (j >= 0) j = s_par[j];
-            }
-            const int64_t at = base + (int64_t)(mine < 0 ? 0 : mine) * tok;
-            r.token(a.k + at, a.v + at, mine >= 0, li, a.scale_log2);
-        }
-        for (int s = grp; s < a.nsplit; s += 4) {
-            const float *pp = a.part + ((row * a.nsplit + s) * a.Hq + h) * (D + 2);
-            float o2[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) o2[e] = pp[li * E + e];
-            r.join(pp[D], pp[D + 1], o2);
-        }
+    const int64_t tok = (int64_t)a.Hkv * D;
+    const int64_t base = (b * a.lens.L_max + sq.P) * tok + (h / a.G) * D;
+    for (int c0 = 0; c0 < s_len; c0 += GROUPS) {
+        const bool on = c0 + grp < s_len;
+        const int64_t at = base + (on ? s_chain[c0 + grp] : 0) * tok;
+        r.token(a.k + at, a.v + at, on, li, a.scale_log2);
     }
+    griddep_wait();  // the prefix parts
+    int64_t x0 = 0, dx = 0;
+    int parts = 0;
+    if (SPARSE) {
+        x0 = row * a.nsplit * a.Hq + h;
+        dx = a.Hq;
+        parts = sq.bad ? 0 : a.nsplit;
+    } else if (sq.P > 0) {
+        const int rr = i * a.G + h % a.G, qt = rr / a.rows;
+        const int64_t u = (b * a.Hkv + h / a.G) * a.units + qt;
+        x0 = (a.first[u] + u) * a.rows + (rr - qt * a.rows);
+        dx = a.rows;
+        parts = a.last[u] - a.first[u] + 1;
+    }
+    for (int s = grp; s < parts; s += GROUPS) {
+        const int64_t x = x0 + s * dx;
+        const float2 ml = *reinterpret_cast<const float2 *>(a.ml + x * 2);
+        float o2[E];
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(a.part + x * D + li * E + e);
+            o2[e] = f.x;
+            o2[e + 1] = f.y;
+            o2[e + 2] = f.z;
+            o2[e + 3] = f.w;
+        }
+        r.join(ml.x, ml.y, o2);
+    }
+    __syncwarp();
     r.join_groups();
-    if (grp == 0) {
-        const float inv = r.l > 0.f ? 1.f / r.l : 0.f;
-        uint16_t *orow = a.o + (row * a.Hq + h) * D + li * E;
+    if (lane < 8) {
 #pragma unroll
-        for (int e = 0; e < E; e += 2)
-            reinterpret_cast<uint32_t *>(orow)[e / 2] = pack_bf16x2(r.o[e] * inv, r.o[e + 1] * inv);
-        if (a.lse && li == 0)
-            a.lse[row * a.Hq + h] = r.l > 0.f ? (r.m + __log2f(r.l)) * LN2 : -INFINITY;
+        for (int e = 0; e < E; ++e) s_o[warp][li * E + e] = r.o[e];
+        if (li == 0) {
+            s_m[warp] = r.m;
+            s_l[warp] = r.l;
+        }
     }
+    __syncthreads();
+    float M = -INFINITY, l = 0.f, o = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) M = fmaxf(M, s_m[w]);
+    const float Mu = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        const float f = fast_exp2(s_m[w] - Mu);
+        l += s_l[w] * f;
+        o += (tid < D ? s_o[w][tid] : 0.f) * f;
+    }
+    if (tid < D) a.o[(row * a.Hq + h) * D + tid] = to_bf16_bits(l == 0.f ? 0.f : o / l);
+    if (a.lse && tid == 0)
+        a.lse[row * a.Hq + h] = l == 0.f ? -INFINITY : (M + __log2f(l)) * LN2;
 }
 
-int splits(int B, int N, int Hq) {
-    const int64_t blocks = (int64_t)B * N * ((Hq + WARPS - 1) / WARPS);
-    int64_t ns = (148 * 8 + blocks - 1) / blocks;
-    return (int)(ns < 1 ? 1 : ns > 32 ? 32 : ns);
+// ------------------------------------------------------------------- host --
+
+// Rows of a unit, units of a (sequence, KV head).
+int unit_tiles(int N, int G) { return N * G > 128 ? 2 : 1; }
+int unit_rows(int N, int G) {
+    const int most = 128 * unit_tiles(N, G);
+    return N * G < most ? N * G : most;
+}
+int unit_count(int N, int G) { return (N * G + unit_rows(N, G) - 1) / unit_rows(N, G); }
+
+struct DenseWs {
+    size_t first, last, part, ml, bytes;
+    DenseWs(int B, int N, int Hkv, int G, int D) {
+        const size_t units = (size_t)B * Hkv * unit_count(N, G);
+        const size_t x = (MAX_CTAS + units) * unit_rows(N, G);
+        first = kWsHeader;
+        last = first + (units * 4 + 255) / 256 * 256;
+        part = last + (units * 4 + 255) / 256 * 256;
+        ml = part + x * D * 4;
+        bytes = ml + x * 8;
+    }
+};
+
+template <int D, int NT>
+cudaError_t run_dense(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, int ctas,
+                      cudaStream_t s) {
+    auto kern = tree_dense_kernel<D, NT>;
+    const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), Cfg<D, NT>::BYTES);
+    if (e != cudaSuccess) return e;
+    kern<<<ctas, THREADS, Cfg<D, NT>::BYTES, s>>>(tk, tv, a);
+    return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t run(const Args &a, int B, cudaStream_t s) {
-    const int64_t rows = (int64_t)B * a.N;
-    const unsigned hy = (a.Hq + WARPS - 1) / WARPS;
-    const dim3 pg((unsigned)(rows * a.nsplit), hy);
-    if (a.sel)
-        tree_prefix_kernel<D, true><<<pg, WARPS * 32, 0, s>>>(a);
-    else
-        tree_prefix_kernel<D, false><<<pg, WARPS * 32, 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    return launch_dependent(tree_merge_kernel<D>, dim3((unsigned)rows, hy), dim3(WARPS * 32), 0, s,
-                            a);
+cudaError_t run_merge(const Args &a, bool sparse, cudaStream_t s) {
+    const dim3 grid((unsigned)((int64_t)a.B * a.N), a.Hq);
+    return sparse ? launch_dependent(tree_merge_kernel<D, true>, grid, dim3(WARPS * 32), 0, s, a)
+                  : launch_dependent(tree_merge_kernel<D, false>, grid, dim3(WARPS * 32), 0, s, a);
 }
 
 }  // namespace tree
 
 int tree_max_drafts() { return tree::MAX_N; }
 
-size_t tree_ws_bytes(int B, int N, int Hq, int D) {
-    return kWsHeader +
-           (size_t)B * N * tree::splits(B, N, Hq) * Hq * (D + 2) * sizeof(float);
+size_t tree_dense_ws_bytes(int B, int N, int Hq, int Hkv, int D) {
+    return tree::DenseWs(B, N, Hkv, Hq / Hkv, D).bytes;
+}
+
+// The split depends on the KV heads, which the size does not: the most of any.
+size_t tree_sparse_ws_bytes(int B, int N, int Hq, int D, int kb) {
+    const int64_t rows = (int64_t)B * N;
+    return kWsHeader + (size_t)rows * tree_sparse_splits(rows, kb, 4) * Hq * (D + 2) * sizeof(float);
 }
 
 cudaError_t launch_tree_decode(const uint16_t *q, const uint16_t *k, const uint16_t *v,
                                const int32_t *seqlens, const int32_t *n_draft, int64_t L_max,
                                const int32_t *sel, int64_t sel_b, int64_t sel_n, int kb,
                                const int32_t *parent, int B, int N, int Hq, int Hkv, int D,
-                               float scale, uint16_t *o, float *lse, void *ws, cudaStream_t s) {
+                               float scale, uint16_t *o, float *lse, void *ws, int num_sms,
+                               cudaStream_t s) {
     tree::Args a{};
+    uint8_t *w = static_cast<uint8_t *>(ws);
     a.q = q; a.k = k; a.v = v; a.lens = tree::Lens{seqlens, n_draft, N, L_max};
-    a.parent = parent; a.sel = sel; a.sel_b = sel_b; a.sel_n = sel_n; a.kb = kb;
-    a.N = N; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.nsplit = tree::splits(B, N, Hq);
-    a.scale_log2 = scale * tree::LOG2E;
-    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kWsHeader);
-    a.o = o; a.lse = lse; a.status = ws;
-    return D == 64 ? tree::run<64>(a, B, s) : tree::run<128>(a, B, s);
+    a.parent = parent; a.B = B; a.N = N; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv;
+    a.scale_log2 = scale * tree::LOG2E; a.o = o; a.lse = lse; a.status = ws;
+    cudaError_t e;
+    if (sel) {
+        a.nsplit = tree_sparse_splits((int64_t)B * N, kb, Hkv);
+        a.part = reinterpret_cast<float *>(w + kWsHeader);
+        a.ml = a.part + (int64_t)B * N * a.nsplit * Hq * D;
+        const TreePrefix t{seqlens, n_draft, N, sel, sel_b, sel_n, a.part, a.ml};
+        e = launch_tree_sparse_prefix(q, k, v, t, L_max, kb, a.nsplit, B, Hq, Hkv, D, scale,
+                                      num_sms, s);
+    } else {
+        const tree::DenseWs x(B, N, Hkv, a.G, D);
+        a.units = tree::unit_count(N, a.G);
+        a.rows = tree::unit_rows(N, a.G);
+        a.first = reinterpret_cast<int32_t *>(w + x.first);
+        a.last = reinterpret_cast<int32_t *>(w + x.last);
+        a.part = reinterpret_cast<float *>(w + x.part);
+        a.ml = reinterpret_cast<float *>(w + x.ml);
+        CUtensorMap tk, tv;
+        if (!tensor_map_cache_bf16(&tk, k, B, L_max, Hkv * D, tree::KT) ||
+            !tensor_map_cache_bf16(&tv, v, B, L_max, Hkv * D, tree::KT))
+            return cudaErrorInvalidValue;
+        const int ctas = num_sms < tree::MAX_CTAS ? num_sms : tree::MAX_CTAS;
+        const bool two = tree::unit_tiles(N, a.G) == 2;
+        if (D == 64)
+            e = two ? tree::run_dense<64, 2>(tk, tv, a, ctas, s)
+                    : tree::run_dense<64, 1>(tk, tv, a, ctas, s);
+        else
+            e = two ? tree::run_dense<128, 2>(tk, tv, a, ctas, s)
+                    : tree::run_dense<128, 1>(tk, tv, a, ctas, s);
+    }
+    if (e != cudaSuccess) return e;
+    return D == 64 ? tree::run_merge<64>(a, sel != nullptr, s)
+                   : tree::run_merge<128>(a, sel != nullptr, s);
 }
 
 }  // namespace qsa
