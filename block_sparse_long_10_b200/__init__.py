@@ -495,31 +495,60 @@ _SCALING = {"none": 0, "linear": 1, "ntk": 2, "by-parts": 3}
 _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
 
 
-def _shape(t, shape, name):
-    if t is not None and tuple(t.shape) != tuple(shape):
+_Tensor = torch.Tensor
+
+
+def _arg(t, dtype, shape, dev, name):
+    """The pointer of a contiguous tensor of this type and shape on device `dev` (None passes).
+    A step of a few microseconds on the GPU passes a dozen tensors: one line tells that all
+    is well, what is wrong is found after it."""
+    if t is None:
+        return None
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.get_device() == dev and dev >= 0):
+        return t.data_ptr()
+    _need(t, dtype, name, len(shape))
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
 
 
-def _rows(t, dtype, name, shape=None):
-    """A [B,T,H,D] CUDA tensor whose tokens lie at one stride, heads packed; the stride."""
-    if not isinstance(t, torch.Tensor):
+def _given(t, name, ndim):
+    """A tensor from whose shape and device the others' follow."""
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
+    return t.get_device()
+
+
+def _space(ws, dev):
+    """The pointer of a workspace, whatever its size."""
+    _given(ws, "ws", 1)
+    return _arg(ws, torch.uint8, ws.shape, dev, "ws")
+
+
+def _rows(t, dtype, shape, dev, name):
+    """(pointer, stride) of a [B,T,H,D] tensor whose tokens lie at one stride, heads packed."""
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 4:
-        raise ValueError(f"{name} must have 4 dims, got {tuple(t.shape)}")
-    if shape is not None:
-        _shape(t, shape, name)
-    B, T, H, D = t.shape
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor on one device with the others, "
+                         f"is on {t.device}")
+    B, T, H, D = shape
+    if t.is_contiguous():
+        return t.data_ptr(), H * D
     sb, st, sh, sd = t.stride()
     if T == 1:
         st = sb if B > 1 else H * D
     if (D > 1 and sd != 1) or (H > 1 and sh != D) or (B > 1 and T > 0 and sb != T * st):
         raise ValueError(f"{name}'s tokens must lie at one stride, its heads packed; "
                          f"strides {t.stride()}")
-    return max(st, H * D) if B * T <= 1 else st
+    return t.data_ptr(), (max(st, H * D) if B * T <= 1 else st)
 
 
 def _layout(layout):
@@ -528,19 +557,17 @@ def _layout(layout):
     return _LAYOUT[layout]
 
 
-def _one_device(first, **others):
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
-
-
-def _call_on(device, name, *args):
-    """_call with `device` current: the library launches on the current device."""
-    if torch.cuda.current_device() == device.index:
-        _call(name, *args)
+def _call_on(dev, stream, name, *args):
+    """_call with device `dev` current (the library launches on the current device) and its
+    current stream, or `stream`, as the last argument."""
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        rc = getattr(_lib or load(), name)(*args, s)
     else:
-        with torch.cuda.device(device):
-            _call(name, *args)
+        with torch.cuda.device(dev):
+            rc = getattr(_lib or load(), name)(*args, s)
+    if rc != 0:
+        raise QSAError(rc, name)
 
 
 def qsa_rope_frequencies(base, rot, scaling="none", factor=1.0, orig_len=0.0, beta_fast=32.0,
@@ -557,19 +584,13 @@ def qsa_rope_frequencies(base, rot, scaling="none", factor=1.0, orig_len=0.0, be
     return (freq if device is None else freq.to(device)), mscale.value
 
 
-def _positions(pos, pos0, B, T):
-    _need(pos, _I64T, "pos", 2)
-    _need(pos0, _I64T, "pos0", 1)
-    _shape(pos, (B, T), "pos")
-    _shape(pos0, (B,), "pos0")
-
-
-def _freq(freq):
+def _freq(freq, dev):
     """(pointer, rot) of a frequency table; None: no rotation."""
     if freq is None:
         return None, 0
-    _need(freq, torch.float64, "freq", 1)
-    return _ptr(freq), 2 * freq.numel()
+    _given(freq, "freq", 1)
+    n = freq.numel()
+    return _arg(freq, torch.float64, (n,), dev, "freq"), 2 * n
 
 
 def qsa_rope(x, y, freq, pos=None, pos0=None, layout="half", mscale=1.0, transpose=False,
@@ -577,17 +598,16 @@ def qsa_rope(x, y, freq, pos=None, pos0=None, layout="half", mscale=1.0, transpo
     """x [B,T,H,D] bf16 or fp32 -> y (same type; may be x): the first 2 * len(freq) dims of
     each head turned by position * freq; transpose: the gradient's map.  Tokens may lie at
     any one stride (a part of a packed projection), heads packed."""
-    if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPE:
+    if not isinstance(x, _Tensor) or x.dtype not in _DTYPE:
         raise TypeError("x must be a torch.bfloat16 or torch.float32 tensor")
-    xs = _rows(x, x.dtype, "x")
-    ys = _rows(y, x.dtype, "y", x.shape)
-    B, T, H, D = x.shape
-    fp, rot = _freq(freq)
-    _positions(pos, pos0, B, T)
-    _one_device(x, y=y, freq=freq, pos=pos, pos0=pos0)
-    _call_on(x.device, "qsa_rope", _ptr(x), xs, _ptr(y), ys, _DTYPE[x.dtype], B, T, H, D, fp, rot,
-             _layout(layout), mscale, int(bool(transpose)), _ptr(pos), _ptr(pos0),
-             _stream(stream, x.device))
+    dev, dt, shape = _given(x, "x", 4), x.dtype, x.shape
+    xp, xs = _rows(x, dt, shape, dev, "x")
+    yp, ys = _rows(y, dt, shape, dev, "y")
+    B, T, H, D = shape
+    fp, rot = _freq(freq, dev)
+    _call_on(dev, stream, "qsa_rope", xp, xs, yp, ys, _DTYPE[dt], B, T, H, D, fp, rot,
+             _layout(layout), mscale, bool(transpose), _arg(pos, _I64T, (B, T), dev, "pos"),
+             _arg(pos0, _I64T, (B,), dev, "pos0"))
 
 
 def qsa_qk_norm_rope(q, k, q_out, k_out, freq, v=None, v_out=None, q_weight=None, k_weight=None,
@@ -597,38 +617,29 @@ def qsa_qk_norm_rope(q, k, q_out, k_out, freq, v=None, v_out=None, q_weight=None
     with slot [B,T] int64 the rows slot of caches [B,L,Hkv,D]: per-head RMS norm (where a
     weight [D] fp32 is given), then the rotation; v is copied.  Inputs may be parts of one
     packed projection.  ws: takes the status word (a slot >= L)."""
-    qs = _rows(q, _BF, "q")
-    ks = _rows(k, _BF, "k")
+    dev = _given(q, "q", 4)
+    qp, qs = _rows(q, _BF, q.shape, dev, "q")
     B, T, Hq, D = q.shape
+    _given(k, "k", 4)
     Hkv = k.shape[2]
-    _shape(k, (B, T, Hkv, D), "k")
-    vs = 0 if v is None else _rows(v, _BF, "v", k.shape)
+    rows = (B, T, Hkv, D)
+    kp, ks = _rows(k, _BF, rows, dev, "k")
+    vp, vs = (None, 0) if v is None else _rows(v, _BF, rows, dev, "v")
     if (v is None) != (v_out is None):
         raise ValueError("v and v_out go together")
-    _need(q_out, _BF, "q_out", 4)
-    _shape(q_out, q.shape, "q_out")
-    _need(k_out, _BF, "k_out", 4)
-    L = k_out.shape[1]
-    _shape(k_out, (B, T if slot is None else L, Hkv, D), "k_out")
-    _need(v_out, _BF, "v_out", 4)
-    _shape(v_out, k_out.shape, "v_out")
-    _need(q_weight, _F32, "q_weight", 1)
-    _need(k_weight, _F32, "k_weight", 1)
-    _shape(q_weight, (D,), "q_weight")
-    _shape(k_weight, (D,), "k_weight")
-    _need(slot, _I64T, "slot", 2)
-    _shape(slot, (B, T), "slot")
-    _need(ws, torch.uint8, "ws", 1)
+    _given(k_out, "k_out", 4)
+    L = T if slot is None else k_out.shape[1]
+    out = (B, L, Hkv, D)
+    wp = None if ws is None else _space(ws, dev)
     if ws is not None and ws.numel() < 256:
         raise ValueError("ws must hold the 256-byte status header")
-    fp, rot = _freq(freq)
-    _positions(pos, pos0, B, T)
-    _one_device(q, k=k, v=v, q_out=q_out, k_out=k_out, v_out=v_out, q_weight=q_weight,
-                k_weight=k_weight, freq=freq, pos=pos, pos0=pos0, slot=slot, ws=ws)
-    _call_on(q.device, "qsa_qk_norm_rope", _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, B, T, Hq, Hkv,
-             D, _ptr(q_weight), _ptr(k_weight), eps, fp, rot, _layout(layout), mscale, _ptr(pos),
-             _ptr(pos0), _ptr(q_out), _ptr(k_out), _ptr(v_out), _ptr(slot), L, _ptr(ws),
-             _stream(stream, q.device))
+    fp, rot = _freq(freq, dev)
+    _call_on(dev, stream, "qsa_qk_norm_rope", qp, qs, kp, ks, vp, vs, B, T, Hq, Hkv, D,
+             _arg(q_weight, _F32, (D,), dev, "q_weight"),
+             _arg(k_weight, _F32, (D,), dev, "k_weight"), eps, fp, rot, _layout(layout), mscale,
+             _arg(pos, _I64T, (B, T), dev, "pos"), _arg(pos0, _I64T, (B,), dev, "pos0"),
+             _arg(q_out, _BF, q.shape, dev, "q_out"), _arg(k_out, _BF, out, dev, "k_out"),
+             _arg(v_out, _BF, out, dev, "v_out"), _arg(slot, _I64T, (B, T), dev, "slot"), L, wp)
 
 
 def qsa_qk_norm_rope_backward_workspace_size(B, T, Hq, Hkv, D) -> int:
@@ -642,57 +653,42 @@ def qsa_qk_norm_rope_backward(d_q, d_k, q, k, dq, dk, freq, ws=None, q_weight=No
     -> dq, dk (bf16 or fp32) of its inputs q, k, and dq_weight, dk_weight [D] fp32 of its
     weights (overwritten), where wanted; ws: for the weight gradients."""
     for t, n in ((d_q, "d_q"), (dq, "dq")):
-        if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPE:
+        if not isinstance(t, _Tensor) or t.dtype not in _DTYPE:
             raise TypeError(f"{n} must be a torch.bfloat16 or torch.float32 tensor")
-    qs = _rows(q, _BF, "q")
-    ks = _rows(k, _BF, "k")
+    dev = _given(q, "q", 4)
+    qp, qs = _rows(q, _BF, q.shape, dev, "q")
     B, T, Hq, D = q.shape
+    _given(k, "k", 4)
     Hkv = k.shape[2]
-    _shape(k, (B, T, Hkv, D), "k")
-    for t, ref, dt, n in ((d_q, q, d_q.dtype, "d_q"), (d_k, k, d_q.dtype, "d_k"),
-                          (dq, q, dq.dtype, "dq"), (dk, k, dq.dtype, "dk")):
-        _need(t, dt, n, 4)
-        _shape(t, ref.shape, n)
-    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight"), (dq_weight, "dq_weight"),
-                 (dk_weight, "dk_weight")):
-        _need(t, _F32, n, 1)
-        _shape(t, (D,), n)
-    _need(ws, torch.uint8, "ws", 1)
-    fp, rot = _freq(freq)
-    _positions(pos, pos0, B, T)
-    _one_device(q, d_q=d_q, d_k=d_k, k=k, dq=dq, dk=dk, q_weight=q_weight, k_weight=k_weight,
-                dq_weight=dq_weight, dk_weight=dk_weight, freq=freq, pos=pos, pos0=pos0, ws=ws)
-    _call_on(q.device, "qsa_qk_norm_rope_backward", _ptr(d_q), _ptr(d_k), _DTYPE[d_q.dtype],
-             _ptr(q), qs, _ptr(k), ks, B, T, Hq, Hkv, D, _ptr(q_weight), _ptr(k_weight), eps, fp,
-             rot, _layout(layout), mscale, _ptr(pos), _ptr(pos0), _ptr(dq), _ptr(dk),
-             _DTYPE[dq.dtype], _ptr(dq_weight), _ptr(dk_weight), _ptr(ws),
-             0 if ws is None else ws.numel(), _stream(stream, q.device))
+    rows = (B, T, Hkv, D)
+    kp, ks = _rows(k, _BF, rows, dev, "k")
+    dt, xt = d_q.dtype, dq.dtype
+    fp, rot = _freq(freq, dev)
+    _call_on(dev, stream, "qsa_qk_norm_rope_backward", _arg(d_q, dt, q.shape, dev, "d_q"),
+             _arg(d_k, dt, rows, dev, "d_k"), _DTYPE[dt], qp, qs, kp, ks, B, T, Hq, Hkv, D,
+             _arg(q_weight, _F32, (D,), dev, "q_weight"),
+             _arg(k_weight, _F32, (D,), dev, "k_weight"), eps, fp, rot, _layout(layout), mscale,
+             _arg(pos, _I64T, (B, T), dev, "pos"), _arg(pos0, _I64T, (B,), dev, "pos0"),
+             _arg(dq, xt, q.shape, dev, "dq"), _arg(dk, xt, rows, dev, "dk"), _DTYPE[xt],
+             _arg(dq_weight, _F32, (D,), dev, "dq_weight"),
+             _arg(dk_weight, _F32, (D,), dev, "dk_weight"),
+             None if ws is None else _space(ws, dev), 0 if ws is None else ws.numel())
 
 
 # ------------------------------------------------ trees of drafted tokens --
 
 def _tree(q, k_cache, v_cache, seqlens, parent, o, ws, n_draft, lse):
-    _need(q, _BF, "q", 4)
-    _need(k_cache, _BF, "k_cache", 4)
-    _need(v_cache, _BF, "v_cache", 4)
-    _need(o, _BF, "o", 4)
-    _need(seqlens, _I32, "seqlens", 1)
-    _need(parent, _I32, "parent", 2)
-    _need(n_draft, _I32, "n_draft", 1)
-    _need(lse, _F32, "lse", 3)
-    _need(ws, torch.uint8, "ws", 1)
+    """Device, sizes and pointers that both tree calls pass."""
+    dev = _given(q, "q", 4)
+    _given(k_cache, "k_cache", 4)
     B, N, Hq, D = q.shape
     L, Hkv = k_cache.shape[1], k_cache.shape[2]
-    _shape(k_cache, (B, L, Hkv, D), "k_cache")
-    _shape(v_cache, k_cache.shape, "v_cache")
-    _shape(o, q.shape, "o")
-    _shape(seqlens, (B,), "seqlens")
-    _shape(parent, (B, N), "parent")
-    _shape(n_draft, (B,), "n_draft")
-    _shape(lse, (B, N, Hq), "lse")
-    _one_device(q, k_cache=k_cache, v_cache=v_cache, seqlens=seqlens, parent=parent, o=o, ws=ws,
-                n_draft=n_draft, lse=lse)
-    return B, N, Hq, Hkv, D, L
+    cache = (B, L, Hkv, D)
+    return (dev, (B, N, Hq, Hkv, D), L, _arg(q, _BF, q.shape, dev, "q"),
+            _arg(k_cache, _BF, cache, dev, "k_cache"), _arg(v_cache, _BF, cache, dev, "v_cache"),
+            _arg(seqlens, _I32, (B,), dev, "seqlens"), _arg(parent, _I32, (B, N), dev, "parent"),
+            _arg(n_draft, _I32, (B,), dev, "n_draft"), _arg(o, _BF, q.shape, dev, "o"),
+            _arg(lse, _F32, (B, N, Hq), dev, "lse"), _space(ws, dev))
 
 
 def qsa_dense_tree_decode_workspace_size(B, N, Hq, Hkv, D) -> int:
@@ -704,11 +700,11 @@ def qsa_dense_tree_decode(q, k_cache, v_cache, seqlens, parent, o, ws, n_draft=N
     """Drafted tokens q [B,N,Hq,D], the last n_draft[b] (default N) of the seqlens[b] rows of
     caches [B,L,Hkv,D], over the whole prefix and each over its chain of parents [B,N]
     (-1: the last committed token) -> o [B,N,Hq,D]."""
-    B, N, Hq, Hkv, D, L = _tree(q, k_cache, v_cache, seqlens, parent, o, ws, n_draft, lse)
-    scale = D ** -0.5 if scale is None else scale
-    _call_on(q.device, "qsa_dense_tree_decode", _ptr(q), _ptr(k_cache), _ptr(v_cache),
-             _ptr(seqlens), L, _ptr(parent), _ptr(n_draft), B, N, Hq, Hkv, D, scale, _ptr(o),
-             _ptr(lse), _ptr(ws), ws.numel(), _stream(stream, q.device))
+    dev, sizes, L, qp, kp, vp, sp, pp, np_, op, lp, wp = _tree(q, k_cache, v_cache, seqlens,
+                                                               parent, o, ws, n_draft, lse)
+    scale = sizes[-1] ** -0.5 if scale is None else scale
+    _call_on(dev, stream, "qsa_dense_tree_decode", qp, kp, vp, sp, L, pp, np_, *sizes, scale, op,
+             lp, wp, ws.numel())
 
 
 def qsa_sparse_tree_decode_workspace_size(B, N, Hq, D, r=4, budget=2048) -> int:
@@ -720,20 +716,20 @@ def qsa_sparse_tree_decode(q, k_cache, v_cache, seqlens, sel, parent, o, ws, n_d
     """qsa_dense_tree_decode with each row's prefix cut to its selected blocks sel
     [B,N,budget//r] int32 (any strides but the last; .expand shares one selection) and the
     tokens after the last complete block."""
-    B, N, Hq, Hkv, D, L = _tree(q, k_cache, v_cache, seqlens, parent, o, ws, n_draft, lse)
-    if not isinstance(sel, torch.Tensor) or sel.dtype != _I32:
+    dev, sizes, L, qp, kp, vp, sp, pp, np_, op, lp, wp = _tree(q, k_cache, v_cache, seqlens,
+                                                               parent, o, ws, n_draft, lse)
+    if not isinstance(sel, _Tensor) or sel.dtype is not _I32:
         raise TypeError("sel must be a torch.int32 tensor")
-    if not sel.is_cuda or sel.dim() != 3:
-        raise ValueError("sel must be a CUDA tensor of 3 dims")
-    _shape(sel, (B, N, budget // r), "sel")
-    if sel.shape[2] > 1 and sel.stride(2) != 1:
+    want = (sizes[0], sizes[1], budget // r)
+    if sel.shape != want or sel.get_device() != dev:
+        raise ValueError(f"sel must be {list(want)} on cuda:{dev}, got {list(sel.shape)} on "
+                         f"{sel.device}")
+    sb, sn, se = sel.stride()
+    if want[2] > 1 and se != 1:
         raise ValueError("sel's entries must be contiguous")
-    _one_device(q, sel=sel)
-    scale = D ** -0.5 if scale is None else scale
-    _call_on(q.device, "qsa_sparse_tree_decode", _ptr(q), _ptr(k_cache), _ptr(v_cache),
-             _ptr(seqlens), L, _ptr(sel), sel.stride(0), sel.stride(1), _ptr(parent),
-             _ptr(n_draft), B, N, Hq, Hkv, D, r, budget, scale, _ptr(o), _ptr(lse), _ptr(ws),
-             ws.numel(), _stream(stream, q.device))
+    scale = sizes[-1] ** -0.5 if scale is None else scale
+    _call_on(dev, stream, "qsa_sparse_tree_decode", qp, kp, vp, sp, L, sel.data_ptr(), sb, sn, pp,
+             np_, *sizes, r, budget, scale, op, lp, wp, ws.numel())
 
 
 def qsa_check_device_status(ws, stream=None) -> int:
