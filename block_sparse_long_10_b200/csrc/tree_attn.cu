@@ -197,6 +197,100 @@ QSA_DEVICE uint32_t ring_v(uint32_t base, int j, int n) {
 
 QSA_DEVICE void soft_sync() { asm volatile("bar.sync 1, %0;\n" ::"n"(SOFT) : "memory"); }
 
+// Packed fp32 pairs.
+QSA_DEVICE uint64_t pair(float a, float b) {
+    uint64_t x;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(x) : "f"(a), "f"(b));
+    return x;
+}
+QSA_DEVICE void unpair(uint64_t x, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(x));
+}
+QSA_DEVICE uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+// Volatile: left to itself the compiler puts a tile's sums off, and keeps 128 addends.
+QSA_DEVICE uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm volatile("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Softmax of one row's 128 scores, of which the first `left` count (MASKED): scores in
+// TMEM at s_tm become bf16 probabilities in its first 64 columns; the row's maximum,
+// sum and (at o_tm, if there is one) O move along.  Whole warps.
+template <int D, bool MASKED>
+QSA_DEVICE void soft_tile(uint32_t s_tm, uint32_t o_tm, float sc, int left, bool has_o, float &m,
+                          float &l) {
+    // The scores are read twice, 32 at a time: all 128 in registers would spill.
+    uint32_t x[2][32];
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    sm100::tmem_ld32_begin(s_tm, x[0]);
+#pragma unroll
+    for (int c = 0; c < KT; c += 32) {
+        uint32_t(&y)[32] = x[(c >> 5) & 1];
+        sm100::tmem_ld32_end(y);
+        sm100::tmem_ld32_begin(s_tm + (c + 32) % KT, x[1 - ((c >> 5) & 1)]);
+        if (MASKED) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (c + e >= left) y[e] = 0xff800000u;  // -inf
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 2)
+            mx[(e >> 1) & 3] = fmaxf(mx[(e >> 1) & 3],
+                                     fmaxf(__uint_as_float(y[e]), __uint_as_float(y[e + 1])));
+    }
+    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+    const bool grow = mt > m + GROWTH;
+    if (__any_sync(0xffffffffu, grow)) {
+        const float mn = grow ? mt : m;
+        const float f = grow ? fast_exp2(m - mn) : 1.f;
+        l *= f;
+        m = mn;
+        if (has_o) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+                uint32_t y[16];
+                sm100::tmem_ld16(o_tm + c, y);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+                sm100::tmem_st16(o_tm + c, y);
+            }
+        }
+    }
+    const float mu = m == -INFINITY ? 0.f : m;
+    const uint64_t sc2 = pair(sc, sc), mu2 = pair(-mu, -mu);
+    uint64_t sum[2] = {0, 0};
+#pragma unroll
+    for (int c = 0; c < KT; c += 32) {
+        uint32_t pk[16];
+        uint32_t(&y)[32] = x[(c >> 5) & 1];
+        sm100::tmem_ld32_end(y);
+        if (c + 32 < KT) sm100::tmem_ld32_begin(s_tm + c + 32, x[1 - ((c >> 5) & 1)]);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+            float p0, p1;
+            unpair(fma2(pair(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), sc2, mu2), p0, p1);
+            p0 = fast_exp2(p0);
+            p1 = fast_exp2(p1);
+            if (MASKED) {  // 0 * -inf at a scale of 0
+                if (c + e >= left) p0 = 0.f;
+                if (c + e + 1 >= left) p1 = 0.f;
+            }
+            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair(p0, p1));
+            pk[e / 2] = pack_bf16x2(p0, p1);
+        }
+        sm100::tmem_st16(s_tm + c / 2, pk);
+    }
+    float a, b;
+    unpair(add2(sum[0], sum[1]), a, b);
+    l += a + b;
+    sm100::tmem_wait_st();
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(THREADS, 1)
     tree_dense_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -285,13 +379,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const int s = t & 1;
                     const uint32_t idx = ring_k<NT>(base, NT == 2 ? t >> 1 : t), slot = idx % SL;
                     if (NT == 1 || s == 0) wait(&full[slot], idx / SL);
-                    const uint32_t qa = qs + (NT == 2 ? s * C::TILE : 0);
-                    const uint32_t ka = ring + slot * C::TILE;
+                    const uint64_t qa =
+                        sm100::smem_desc_kmajor(qs + (NT == 2 ? s * C::TILE : 0), 128);
+                    const uint64_t ka = sm100::smem_desc_kmajor(ring + slot * C::TILE, 128);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = (k >> 2) * ATOM + (k & 3) * 32;
-                        sm100::mma_bf16(tmem + s * KT, sm100::smem_desc_kmajor(qa + off, 128),
-                                        sm100::smem_desc_kmajor(ka + off, 128), C::IDESC_S, k > 0);
+                        const uint32_t off = ((k >> 2) * ATOM + (k & 3) * 32) >> 4;
+                        sm100::mma_bf16(tmem + s * KT, qa + off, ka + off, C::IDESC_S, k > 0);
                     }
                     sm100::mma_commit(&sfull[s]);
                     if (NT == 1 || s == 1) sm100::mma_commit(&empty[slot]);
@@ -305,12 +399,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                     wait(&pready[s], done[s]++);
                     if (NT == 1 || s == 0) wait(&full[slot], idx / SL);
                     sm100::tc_fence_after();
-                    const uint32_t va = ring + slot * C::TILE;
+                    const uint64_t va = sm100::smem_desc_mnmajor(ring + slot * C::TILE, ATOM);
 #pragma unroll
                     for (int k = 0; k < KT / 16; ++k)
                         sm100::mma_bf16_ta(tmem + C::O_COL + s * D, tmem + s * KT + k * 8,
-                                           sm100::smem_desc_mnmajor(va + k * 2048, ATOM),
-                                           C::IDESC_O, t > 1 || k > 0);
+                                           va + k * (2048 >> 4), C::IDESC_O, t > 1 || k > 0);
                     if (NT == 1 || s == 1) sm100::mma_commit(&empty[slot]);
                     if (t + 2 < steps) scores(t + 2);
                 }
@@ -360,56 +453,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 wait(&sfull[s], got++);
                 sm100::tc_fence_after();
                 if (on) {
-                    uint32_t x[KT];
-                    sm100::tmem_ld128(s_tm, x);
-                    if (left < KT) {
-#pragma unroll
-                        for (int c = 0; c < KT; ++c)
-                            if (c >= left) x[c] = 0xff800000u;  // -inf
-                    }
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int c = 0; c < KT; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(x[c]));
-                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-                    const bool grow = mt > m + GROWTH;
-                    if (__any_sync(0xffffffffu, grow)) {
-                        const float mn = grow ? mt : m;
-                        const float f = grow ? fast_exp2(m - mn) : 1.f;
-                        l *= f;
-                        m = mn;
-                        if (t > 1) {
-#pragma unroll
-                            for (int c = 0; c < D; c += 32) {
-                                uint32_t y[32];
-                                sm100::tmem_ld32(o_tm + c, y);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
-                                sm100::tmem_st32(o_tm + c, y);
-                            }
-                        }
-                    }
-                    const float mu = m == -INFINITY ? 0.f : m;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int c = 0; c < KT; c += 32) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float p0 = fast_exp2(fmaf(__uint_as_float(x[c + e]), sc, -mu));
-                            float p1 = fast_exp2(fmaf(__uint_as_float(x[c + e + 1]), sc, -mu));
-                            if (left < KT) {  // 0 * -inf at a scale of 0
-                                if (c + e >= left) p0 = 0.f;
-                                if (c + e + 1 >= left) p1 = 0.f;
-                            }
-                            sum[e & 2] += p0;
-                            sum[(e & 2) + 1] += p1;
-                            pk[e / 2] = pack_bf16x2(p0, p1);
-                        }
-                        sm100::tmem_st16(s_tm + c / 2, pk);
-                    }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    sm100::tmem_wait_st();
+                    if (left < KT)
+                        soft_tile<D, true>(s_tm, o_tm, sc, (int)left, t > 1, m, l);
+                    else
+                        soft_tile<D, false>(s_tm, o_tm, sc, KT, t > 1, m, l);
                 }
                 if (left < KT && (NT == 1 || s == 0)) {
                     // rows behind the prefix may hold anything: 0 * V must be 0
