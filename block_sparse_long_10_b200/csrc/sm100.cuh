@@ -110,6 +110,17 @@ QSA_DEVICE void prefetch_tensormap(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
+// One lane of the (whole) warp, the same on every call.
+QSA_DEVICE bool elect_one() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok));
+    return ok != 0;
+}
+
 // ----------------------------------------------------------------- tcgen05 --
 QSA_DEVICE void tmem_alloc(uint32_t *slot, uint32_t ncols) {  // whole warp
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(

@@ -368,20 +368,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     } else if (warp == SOFT / 32 + 1) {
         // ----------------------------------------------------------- MMA --
-        if (lane == 0) {
-            const uint32_t qs = smem_u32(sm);
-            uint32_t base = 0, done[2] = {0, 0}, segs = 0;
-            while (walk.next(a, sg)) {
-                const int steps = NT * sg.n;
-                wait(qready, segs);
-                sm100::tc_fence_after();
-                auto scores = [&](int t) {
-                    const int s = t & 1;
-                    const uint32_t idx = ring_k<NT>(base, NT == 2 ? t >> 1 : t), slot = idx % SL;
-                    if (NT == 1 || s == 0) wait(&full[slot], idx / SL);
-                    const uint64_t qa =
-                        sm100::smem_desc_kmajor(qs + (NT == 2 ? s * C::TILE : 0), 128);
-                    const uint64_t ka = sm100::smem_desc_kmajor(ring + slot * C::TILE, 128);
+        // The whole warp walks and waits, so that descriptors stay in uniform registers;
+        // one lane issues.
+        const bool leader = sm100::elect_one();
+        const uint32_t qs = smem_u32(sm);
+        uint32_t base = 0, done[2] = {0, 0}, segs = 0;
+        while (walk.next(a, sg)) {
+            const int n = __shfl_sync(0xffffffffu, sg.n, 0), steps = NT * n;
+            wait(qready, segs);
+            sm100::tc_fence_after();
+            auto scores = [&](int t) {
+                const int s = t & 1;
+                const uint32_t idx = ring_k<NT>(base, NT == 2 ? t >> 1 : t), slot = idx % SL;
+                if (NT == 1 || s == 0) wait(&full[slot], idx / SL);
+                const uint64_t qa = sm100::smem_desc_kmajor(qs + (NT == 2 ? s * C::TILE : 0), 128);
+                const uint64_t ka = sm100::smem_desc_kmajor(ring + slot * C::TILE, 128);
+                if (leader) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint32_t off = ((k >> 2) * ATOM + (k & 3) * 32) >> 4;
@@ -389,28 +391,29 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                     sm100::mma_commit(&sfull[s]);
                     if (NT == 1 || s == 1) sm100::mma_commit(&empty[slot]);
-                };
-                scores(0);
-                if (steps > 1) scores(1);
-                for (int t = 0; t < steps; ++t) {
-                    const int s = t & 1;
-                    const uint32_t idx = ring_v<NT>(base, NT == 2 ? t >> 1 : t, sg.n);
-                    const uint32_t slot = idx % SL;
-                    wait(&pready[s], done[s]++);
-                    if (NT == 1 || s == 0) wait(&full[slot], idx / SL);
-                    sm100::tc_fence_after();
-                    const uint64_t va = sm100::smem_desc_mnmajor(ring + slot * C::TILE, ATOM);
+                }
+            };
+            scores(0);
+            if (steps > 1) scores(1);
+            for (int t = 0; t < steps; ++t) {
+                const int s = t & 1;
+                const uint32_t idx = ring_v<NT>(base, NT == 2 ? t >> 1 : t, n), slot = idx % SL;
+                wait(&pready[s], done[s]++);
+                if (NT == 1 || s == 0) wait(&full[slot], idx / SL);
+                sm100::tc_fence_after();
+                const uint64_t va = sm100::smem_desc_mnmajor(ring + slot * C::TILE, ATOM);
+                if (leader) {
 #pragma unroll
                     for (int k = 0; k < KT / 16; ++k)
                         sm100::mma_bf16_ta(tmem + C::O_COL + s * D, tmem + s * KT + k * 8,
                                            va + k * (2048 >> 4), C::IDESC_O, t > 1 || k > 0);
                     if (NT == 1 || s == 1) sm100::mma_commit(&empty[slot]);
-                    if (t + 2 < steps) scores(t + 2);
                 }
-                sm100::mma_commit(odone);
-                base += 2 * sg.n;
-                ++segs;
+                if (t + 2 < steps) scores(t + 2);
             }
+            if (leader) sm100::mma_commit(odone);
+            base += 2 * n;
+            ++segs;
         }
     } else {
         // ------------------------------------------------------- softmax --
