@@ -52,7 +52,7 @@ struct Args {
     const uint16_t *v;
     Lens lens;
     const int32_t *parent;  // [B, N]
-    int B, N, Hq, Hkv, G;
+    int B, N, Hq, Hkv, G, lg;  // lg: log2 G
     float scale_log2;
     // prefix parts: part x holds O[x * D ..] and (max, sum)[x * 2 ..]
     float *part, *ml;
@@ -196,6 +196,13 @@ QSA_DEVICE uint32_t ring_v(uint32_t base, int j, int n) {
 }
 
 QSA_DEVICE void soft_sync() { asm volatile("bar.sync 1, %0;\n" ::"n"(SOFT) : "memory"); }
+
+// A thread's 32-byte sector in one store.
+QSA_DEVICE void store_sector(float *p, const uint32_t *r) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 
 // Packed fp32 pairs.
 QSA_DEVICE uint64_t pair(float a, float b) {
@@ -422,22 +429,34 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t s_tm = tmem + lanes + s * KT, o_tm = tmem + lanes + C::O_COL + s * D;
         const float sc = fabsf(a.scale_log2);
         const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // the sign moves into Q
+        constexpr int QB = D / 16;  // loads in flight
         float2 *s_ml = reinterpret_cast<float2 *>(sm);  // [2][128]: the query tile, once done with
         uint32_t base = 0, got = 0, segs = 0;
         while (walk.next(a, sg)) {
             const int steps = NT * sg.n;
             const int R = sg.nd * a.G, r0 = sg.qt * 128 * NT;
+            const uint16_t *qb = a.q + (sg.b * a.N * a.Hq + sg.g * a.G) * D;
             if (segs > 0) soft_sync();  // the sums have been read
-            for (int i = tid; i < NT * 128 * (D / 8); i += SOFT) {
-                const int row = i / (D / 8), ch = i % (D / 8);
-                const int rr = r0 + row, d = rr / a.G;
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (rr < R)
-                    x = *reinterpret_cast<const uint4 *>(
-                        a.q + ((sg.b * a.N + d) * a.Hq + sg.g * a.G + (rr - d * a.G)) * D + ch * 8);
-                x.x ^= flip; x.y ^= flip; x.z ^= flip; x.w ^= flip;
-                *reinterpret_cast<uint4 *>(sm + (row >> 7) * C::TILE + (ch >> 3) * ATOM +
-                                           (row & 127) * 128 + (((ch ^ row) & 7) << 4)) = x;
+            // all of a thread's loads at once: one after the other they took 7 us
+#pragma unroll 1
+            for (int i0 = tid; i0 < NT * 128 * (D / 8); i0 += SOFT * QB) {
+                uint4 x[QB];
+#pragma unroll
+                for (int e = 0; e < QB; ++e) {
+                    const int i = i0 + e * SOFT, rr = r0 + i / (D / 8);
+                    x[e] = make_uint4(0, 0, 0, 0);
+                    if (rr < R)
+                        x[e] = *reinterpret_cast<const uint4 *>(
+                            qb + ((int64_t)(rr >> a.lg) * a.Hq + (rr & (a.G - 1))) * D +
+                            i % (D / 8) * 8);
+                }
+#pragma unroll
+                for (int e = 0; e < QB; ++e) {
+                    const int i = i0 + e * SOFT, row = i / (D / 8), ch = i % (D / 8);
+                    x[e].x ^= flip; x[e].y ^= flip; x[e].z ^= flip; x[e].w ^= flip;
+                    *reinterpret_cast<uint4 *>(sm + (row >> 7) * C::TILE + (ch >> 3) * ATOM +
+                                               (row & 127) * 128 + (((ch ^ row) & 7) << 4)) = x[e];
+                }
             }
             sm100::fence_async_shared();
             sm100::tc_fence_before();
@@ -490,9 +509,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         sm100::tmem_ld32(o_tm + c, y);
                         if (row < R)
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                *reinterpret_cast<uint4 *>(out + c + e) =
-                                    make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                            for (int e = 0; e < 32; e += 8) store_sector(out + c + e, y + e);
                     }
                     if (row < R)
                         *reinterpret_cast<float2 *>(a.ml + (slot_row + s * 128 + r) * 2) =
@@ -523,9 +540,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                                    __uint_as_float(z[e]) * f1);
                         if (row < R)
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                *reinterpret_cast<uint4 *>(out + c + e) =
-                                    make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                            for (int e = 0; e < 32; e += 8) store_sector(out + c + e, y + e);
                     }
                     if (row < R && s == 0)
                         *reinterpret_cast<float2 *>(a.ml + (slot_row + r) * 2) =
@@ -551,20 +566,28 @@ struct Row {
     float q[E], o[E];
     float m, l;
 
-    QSA_DEVICE static void load16(const uint16_t *p, float (&f)[E]) {
+    struct Raw {
+        uint4 v[E / 8];
+        QSA_DEVICE void load(const uint16_t *p) {
 #pragma unroll
-        for (int i = 0; i < E / 8; ++i) {
-            const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            for (int i = 0; i < E / 8; ++i) v[i] = reinterpret_cast<const uint4 *>(p)[i];
+        }
+        QSA_DEVICE void get(float (&f)[E]) const {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                f[8 * i + 2 * j] = bf16_lo(w[j]);
-                f[8 * i + 2 * j + 1] = bf16_hi(w[j]);
+            for (int i = 0; i < E / 8; ++i) {
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    f[8 * i + 2 * j] = bf16_lo(w[j]);
+                    f[8 * i + 2 * j + 1] = bf16_hi(w[j]);
+                }
             }
         }
-    }
+    };
     QSA_DEVICE void start(const uint16_t *qrow, int li) {
-        load16(qrow + li * E, q);
+        Raw x;
+        x.load(qrow + li * E);
+        x.get(q);
         m = -INFINITY;
         l = 0.f;
 #pragma unroll
@@ -580,29 +603,19 @@ struct Row {
         for (int e = 0; e < E; ++e) o[e] = o[e] * fa + o2[e] * fb;
         m = mn;
     }
-    // token with cache rows k and v; `on` false: the group sits out (all lanes call)
-    QSA_DEVICE void token(const uint16_t *k, const uint16_t *v, bool on, int li,
-                          float scale_log2) {
-        float f[E], w[E];
+    // a token's cache rows; `on` false: the group sits out (all lanes call)
+    QSA_DEVICE void token(const Raw &k, const Raw &v, bool on, float scale_log2) {
+        float f[E];
         float x = 0.f;
-        if (on) {
-            load16(k + li * E, f);
-            load16(v + li * E, w);
+        k.get(f);
 #pragma unroll
-            for (int e = 0; e < E; ++e) x += q[e] * f[e];
-        }
+        for (int e = 0; e < E; ++e) x += q[e] * f[e];
         x += __shfl_xor_sync(0xffffffffu, x, 1);
         x += __shfl_xor_sync(0xffffffffu, x, 2);
         x += __shfl_xor_sync(0xffffffffu, x, 4);
         if (!on) return;
-        x *= scale_log2;
-        const float mn = fmaxf(m, x);
-        const float mu = mn == -INFINITY ? 0.f : mn;
-        const float fa = fast_exp2(m - mu), p = fast_exp2(x - mu);
-        l = l * fa + p;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * fa + p * w[e];
-        m = mn;
+        v.get(f);
+        join(x * scale_log2, 1.f, f);
     }
     // the warp's four groups' parts become one, in every lane
     QSA_DEVICE void join_groups() {
@@ -618,53 +631,63 @@ struct Row {
     }
 };
 
-constexpr int WARPS = 4;
-
-// A block per (row, head): its 16 groups of 8 lanes share out the chain's tokens, then
-// (after the prefix kernel) the prefix parts.  Runs of 74 parts (one long sequence over
-// all SMs) and of 1 take the same path; the chain is done under the prefix kernel's tail.
-template <int D, bool SPARSE>
-__global__ void __launch_bounds__(WARPS * 32) tree_merge_kernel(const Args a) {
-    constexpr int E = Row<D>::E, GROUPS = WARPS * 4;
-    __shared__ int s_par[MAX_N], s_chain[MAX_N];
-    __shared__ int s_len;
-    __shared__ float s_o[WARPS][D], s_m[WARPS], s_l[WARPS];
+// W warps per (row, head): their 4 W groups of 8 lanes share out the chain's tokens and
+// (after the prefix kernel) the prefix parts, the next ones' loads under the current
+// ones' arithmetic.  W = 1 takes the heads of one KV head into a block, whose loads of
+// the chain meet in L1.
+template <int D, bool SPARSE, int W>
+__global__ void __launch_bounds__(256) tree_merge_kernel(const Args a) {
+    constexpr int E = Row<D>::E;
+    __shared__ float s_o[W > 1 ? W : 1][W > 1 ? D : 1], s_m[W], s_l[W];
     const int64_t row = blockIdx.x;
     const int64_t b = row / a.N;
-    const int i = (int)(row - b * a.N), h = blockIdx.y;
-    const Seq sq = a.lens.at(b);
+    const int i = (int)(row - b * a.N);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, li = lane & 7;
-    const int grp = tid >> 3;
+    const int h = W > 1 ? (int)blockIdx.y : (int)(blockIdx.y * (blockDim.x >> 5)) + warp;
+    const int grp = (W > 1 ? warp * 4 : 0) + (lane >> 3);
+    const Seq sq = a.lens.at(b);
+    const int32_t *parent = a.parent + b * a.N;
     if (sq.bad) {
-        if (i == 0 && h == 0 && tid == 0) record_status(a.status, QSA_ERR_DEVICE);
+        if (i == 0 && h == 0 && lane == 0) record_status(a.status, QSA_ERR_DEVICE);
     } else if (i >= sq.n) {
         return;
     }
-    // a parent must come before its child; any other value ends the chain
-    for (int j = tid; j <= i && j < sq.n; j += WARPS * 32) {
-        int p = a.parent[b * a.N + j];
-        if (p < -1 || p >= j) {
-            record_status(a.status, QSA_ERR_DEVICE);
-            p = -1;
-        }
-        s_par[j] = p;
-    }
-    __syncthreads();
-    if (tid == 0) {
-        int len = 0;
-        if (!sq.bad)
-            for (int j = i; j >= 0; j = s_par[j]) s_chain[len++] = j;
-        s_len = len;
-    }
-    __syncthreads();
     Row<D> r;
     r.start(a.q + (row * a.Hq + h) * D, li);
     const int64_t tok = (int64_t)a.Hkv * D;
-    const int64_t base = (b * a.lens.L_max + sq.P) * tok + (h / a.G) * D;
-    for (int c0 = 0; c0 < s_len; c0 += GROUPS) {
-        const bool on = c0 + grp < s_len;
-        const int64_t at = base + (on ? s_chain[c0 + grp] : 0) * tok;
-        r.token(a.k + at, a.v + at, on, li, a.scale_log2);
+    const int64_t base = (b * a.lens.L_max + sq.P) * tok + (h >> a.lg) * D + li * E;
+    int j = sq.bad ? -1 : i;
+    // the next 4 W drafts of the chain: this group's, or -1.  A parent must come before
+    // its child; any other value ends the chain.
+    auto walk = [&]() {
+        int mine = -1;
+        for (int s = 0; s < 4 * W && j >= 0; ++s) {
+            if (s == grp) mine = j;
+            const int p = parent[j];
+            const bool wrong = p < -1 || p >= j;
+            if (wrong && j == i && lane == 0) record_status(a.status, QSA_ERR_DEVICE);
+            j = wrong ? -1 : p;
+        }
+        return mine;
+    };
+    {
+        int mine = walk();
+        typename Row<D>::Raw k, v;
+        const int64_t at0 = base + (mine < 0 ? 0 : mine) * tok;
+        if (mine >= 0) {
+            k.load(a.k + at0);
+            v.load(a.v + at0);
+        }
+        while (__any_sync(0xffffffffu, mine >= 0)) {
+            const typename Row<D>::Raw k1 = k, v1 = v;
+            const bool on = mine >= 0;
+            mine = walk();
+            if (mine >= 0) {
+                k.load(a.k + base + mine * tok);
+                v.load(a.v + base + mine * tok);
+            }
+            r.token(k1, v1, on, a.scale_log2);
+        }
     }
     griddep_wait();  // the prefix parts
     int64_t x0 = 0, dx = 0;
@@ -674,50 +697,77 @@ __global__ void __launch_bounds__(WARPS * 32) tree_merge_kernel(const Args a) {
         dx = a.Hq;
         parts = sq.bad ? 0 : a.nsplit;
     } else if (sq.P > 0) {
-        const int rr = i * a.G + h % a.G, qt = rr / a.rows;
-        const int64_t u = (b * a.Hkv + h / a.G) * a.units + qt;
-        x0 = (a.first[u] + u) * a.rows + (rr - qt * a.rows);
+        const int rr = (i << a.lg) + (h & (a.G - 1)), qt = rr / a.rows;
+        const int64_t u = (b * a.Hkv + (h >> a.lg)) * a.units + qt;
+        const int first = a.first[u];
+        x0 = (first + u) * a.rows + (rr - qt * a.rows);
         dx = a.rows;
-        parts = a.last[u] - a.first[u] + 1;
+        parts = a.last[u] - first + 1;
     }
-    for (int s = grp; s < parts; s += GROUPS) {
+    float2 ml;
+    float4 f[E / 4];
+    auto fetch = [&](int s) {
         const int64_t x = x0 + s * dx;
-        const float2 ml = *reinterpret_cast<const float2 *>(a.ml + x * 2);
-        float o2[E];
+        ml = *reinterpret_cast<const float2 *>(a.ml + x * 2);
 #pragma unroll
-        for (int e = 0; e < E; e += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(a.part + x * D + li * E + e);
-            o2[e] = f.x;
-            o2[e + 1] = f.y;
-            o2[e + 2] = f.z;
-            o2[e + 3] = f.w;
+        for (int e = 0; e < E / 4; ++e)
+            f[e] = reinterpret_cast<const float4 *>(a.part + x * D + li * E)[e];
+    };
+    if (grp < parts) fetch(grp);
+    for (int s = grp; s < parts; s += 4 * W) {
+        float o2[E];
+        const float2 c = ml;
+#pragma unroll
+        for (int e = 0; e < E / 4; ++e) {
+            o2[4 * e] = f[e].x;
+            o2[4 * e + 1] = f[e].y;
+            o2[4 * e + 2] = f[e].z;
+            o2[4 * e + 3] = f[e].w;
         }
-        r.join(ml.x, ml.y, o2);
+        if (s + 4 * W < parts) fetch(s + 4 * W);
+        r.join(c.x, c.y, o2);
     }
     __syncwarp();
     r.join_groups();
-    if (lane < 8) {
+    if (W > 1) {
+        if (lane < 8) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) s_o[warp][li * E + e] = r.o[e];
-        if (li == 0) {
-            s_m[warp] = r.m;
-            s_l[warp] = r.l;
+            for (int e = 0; e < E; ++e) s_o[warp][li * E + e] = r.o[e];
+            if (li == 0) {
+                s_m[warp] = r.m;
+                s_l[warp] = r.l;
+            }
         }
-    }
-    __syncthreads();
-    float M = -INFINITY, l = 0.f, o = 0.f;
+        __syncthreads();
+        if (warp != 0) return;
+        // group g of warp 0 takes the sums of warps g, g + 4, ...
+        r.m = -INFINITY;
+        r.l = 0.f;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) M = fmaxf(M, s_m[w]);
-    const float Mu = M == -INFINITY ? 0.f : M;
+        for (int e = 0; e < E; ++e) r.o[e] = 0.f;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-        const float f = fast_exp2(s_m[w] - Mu);
-        l += s_l[w] * f;
-        o += (tid < D ? s_o[w][tid] : 0.f) * f;
+        for (int w = 0; w < W; w += 4) {
+            float o2[E];
+            const int ww = w + (lane >> 3);
+#pragma unroll
+            for (int e = 0; e < E; ++e) o2[e] = s_o[ww][li * E + e];
+            r.join(s_m[ww], s_l[ww], o2);
+        }
+        r.join_groups();
     }
-    if (tid < D) a.o[(row * a.Hq + h) * D + tid] = to_bf16_bits(l == 0.f ? 0.f : o / l);
-    if (a.lse && tid == 0)
-        a.lse[row * a.Hq + h] = l == 0.f ? -INFINITY : (M + __log2f(l)) * LN2;
+    if (lane < 8) {
+        const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
+        uint16_t *orow = a.o + (row * a.Hq + h) * D + li * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 8)
+            *reinterpret_cast<uint4 *>(orow + e) =
+                make_uint4(pack_bf16x2(r.o[e] * inv, r.o[e + 1] * inv),
+                           pack_bf16x2(r.o[e + 2] * inv, r.o[e + 3] * inv),
+                           pack_bf16x2(r.o[e + 4] * inv, r.o[e + 5] * inv),
+                           pack_bf16x2(r.o[e + 6] * inv, r.o[e + 7] * inv));
+        if (a.lse && li == 0)
+            a.lse[row * a.Hq + h] = r.l == 0.f ? -INFINITY : (r.m + __log2f(r.l)) * LN2;
+    }
 }
 
 // ------------------------------------------------------------------- host --
@@ -753,11 +803,15 @@ cudaError_t run_dense(const CUtensorMap &tk, const CUtensorMap &tv, const Args &
     return cudaGetLastError();
 }
 
-template <int D>
-cudaError_t run_merge(const Args &a, bool sparse, cudaStream_t s) {
-    const dim3 grid((unsigned)((int64_t)a.B * a.N), a.Hq);
-    return sparse ? launch_dependent(tree_merge_kernel<D, true>, grid, dim3(WARPS * 32), 0, s, a)
-                  : launch_dependent(tree_merge_kernel<D, false>, grid, dim3(WARPS * 32), 0, s, a);
+// Few (row, head) pairs (under 8 warps an SM) have many parts each: 8 warps a pair.
+template <int D, bool SPARSE>
+cudaError_t run_merge(const Args &a, cudaStream_t s) {
+    const int64_t rows = (int64_t)a.B * a.N;
+    if (rows * a.Hq < 148 * 8)
+        return launch_dependent(tree_merge_kernel<D, SPARSE, 8>, dim3((unsigned)rows, a.Hq),
+                                dim3(256), 0, s, a);
+    return launch_dependent(tree_merge_kernel<D, SPARSE, 1>, dim3((unsigned)rows, a.Hkv),
+                            dim3(a.G * 32), 0, s, a);
 }
 
 }  // namespace tree
@@ -784,6 +838,7 @@ cudaError_t launch_tree_decode(const uint16_t *q, const uint16_t *k, const uint1
     uint8_t *w = static_cast<uint8_t *>(ws);
     a.q = q; a.k = k; a.v = v; a.lens = tree::Lens{seqlens, n_draft, N, L_max};
     a.parent = parent; a.B = B; a.N = N; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv;
+    while (1 << a.lg < a.G) ++a.lg;  // 1, 2, 4 or 8 heads to a KV head
     a.scale_log2 = scale * tree::LOG2E; a.o = o; a.lse = lse; a.status = ws;
     cudaError_t e;
     if (sel) {
@@ -815,8 +870,8 @@ cudaError_t launch_tree_decode(const uint16_t *q, const uint16_t *k, const uint1
                     : tree::run_dense<128, 1>(tk, tv, a, ctas, s);
     }
     if (e != cudaSuccess) return e;
-    return D == 64 ? tree::run_merge<64>(a, sel != nullptr, s)
-                   : tree::run_merge<128>(a, sel != nullptr, s);
+    if (sel) return D == 64 ? tree::run_merge<64, true>(a, s) : tree::run_merge<128, true>(a, s);
+    return D == 64 ? tree::run_merge<64, false>(a, s) : tree::run_merge<128, false>(a, s);
 }
 
 }  // namespace qsa
