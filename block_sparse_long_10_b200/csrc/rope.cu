@@ -150,11 +150,6 @@ QSA_DEVICE void rotate(float (&a)[VEC], float (&b)[VEC], const float (&c)[VEC],
     }
 }
 
-QSA_DEVICE float group_sum(float x, int lanes) {
-    for (int o = lanes >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-}
-
 template <int VEC>
 QSA_DEVICE void load_weight(const float *w, int d, float (&f)[VEC]) {
 #pragma unroll
@@ -234,10 +229,187 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const RopeArgs a) {
 }
 
 // ---------------------------------------------------- norm and rotation --
+// Both kernels below stream rows (one head of one token): a group of lanes takes an item
+// (a token's run of rows) and its rows one after the other, so that one set of angles
+// serves all of them.  A row's vectors come through a ring in shared memory that belongs
+// to the thread alone (cp.async, no barrier), STAGES rows deep: registers hold one row,
+// and enough bytes are in flight for HBM whatever the occupancy.  The arithmetic is in
+// packed pairs of fp32: unpacked it took half of the issue slots and the time of the loads.
+// Before, with 4 rows in registers: 84 us for 32K tokens forward (16 + 2 heads of 128),
+// 195 us backward with fp32 gradients.
+
+// Packed fp32 pairs.
+struct F2 {
+    uint64_t v;
+};
+QSA_DEVICE F2 pack2(float a, float b) {
+    F2 x;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(x.v) : "f"(a), "f"(b));
+    return x;
+}
+QSA_DEVICE float2 unpack2(F2 x) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(f.x), "=f"(f.y) : "l"(x.v));
+    return f;
+}
+QSA_DEVICE F2 swap2(F2 x) {
+    const float2 f = unpack2(x);
+    return pack2(f.y, f.x);
+}
+QSA_DEVICE F2 fma2(F2 a, F2 b, F2 c) {
+    F2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return d;
+}
+QSA_DEVICE F2 mul2(F2 a, F2 b) {
+    F2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+QSA_DEVICE float sum2(F2 x) {
+    const float2 f = unpack2(x);
+    return f.x + f.y;
+}
+
+// VEC elements as they lie in memory; cp.async into shared memory and back.
+template <typename T, int VEC>
+struct Line {
+    static constexpr int BYTES = VEC * (int)sizeof(T);
+    uint32_t w[BYTES / 4];
+    QSA_DEVICE static void copy(uint32_t dst, const T *src) {
+        if (BYTES == 8)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(dst), "l"(src));
+        else
+#pragma unroll
+            for (int i = 0; i < BYTES / 16; ++i)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst + i * 16),
+                             "l"(src + i * (16 / (int)sizeof(T))));
+    }
+    QSA_DEVICE void fetch(const uint8_t *p) {
+        if (BYTES == 8) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(p);
+            w[0] = v.x;
+            w[1] = v.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < BYTES / 16; ++i) {
+                const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
+                w[4 * i] = v.x;
+                w[4 * i + 1] = v.y;
+                w[4 * i + 2] = v.z;
+                w[4 * i + 3] = v.w;
+            }
+        }
+    }
+    QSA_DEVICE void store(T *p) const {
+        if (BYTES == 8)
+            *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+        else
+#pragma unroll
+            for (int i = 0; i < BYTES / 16; ++i)
+                reinterpret_cast<uint4 *>(p)[i] =
+                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    QSA_DEVICE F2 get(int i) const {  // elements 2 i and 2 i + 1
+        if (sizeof(T) == 2) return pack2(bf16_lo(w[i]), bf16_hi(w[i]));
+        return pack2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    }
+    QSA_DEVICE void set(int i, F2 x) {
+        const float2 f = unpack2(x);
+        if (sizeof(T) == 2) {
+            w[i] = pack_bf16x2(f.x, f.y);
+        } else {
+            w[2 * i] = __float_as_uint(f.x);
+            w[2 * i + 1] = __float_as_uint(f.y);
+        }
+    }
+};
+
+// A lane's turned pair of vectors: a' = k0 a + k1 x, b' = k2 b + k3 y, where (x, y) is
+// (b, a) in the half layout and (a, b) with each pair swapped in the interleaved one.
+// Lanes beyond the rotated dims only scale by k0 and k2: a zero times the other half's
+// infinity must not reach them.
+template <int VEC, bool HALF>
+struct Turn {
+    F2 k0[VEC / 2], k1[VEC / 2], k2[VEC / 2], k3[VEC / 2];
+    // cosines and sines of the lane's pairs (sines negated for the transpose), times what
+    // each element is scaled by before it is turned
+    QSA_DEVICE void set(const float (&c)[VEC], const float (&s)[VEC], const float (&wa)[VEC],
+                        const float (&wb)[VEC], bool turns) {
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+            const int e = 2 * i, f = 2 * i + 1;
+            if (!turns) {
+                k0[i] = pack2(wa[e], wa[f]);
+                k2[i] = pack2(wb[e], wb[f]);
+                k1[i] = k3[i] = pack2(0.f, 0.f);
+            } else if (HALF) {
+                k0[i] = pack2(c[e] * wa[e], c[f] * wa[f]);
+                k1[i] = pack2(-s[e] * wb[e], -s[f] * wb[f]);
+                k2[i] = pack2(c[e] * wb[e], c[f] * wb[f]);
+                k3[i] = pack2(s[e] * wa[e], s[f] * wa[f]);
+            } else {
+                const float ca = c[i], sa = s[i], cb = c[VEC / 2 + i], sb = s[VEC / 2 + i];
+                k0[i] = pack2(ca * wa[e], ca * wa[f]);
+                k1[i] = pack2(-sa * wa[f], sa * wa[e]);
+                k2[i] = pack2(cb * wb[e], cb * wb[f]);
+                k3[i] = pack2(-sb * wb[f], sb * wb[e]);
+            }
+        }
+    }
+    QSA_DEVICE void apply(int i, F2 a, F2 b, bool turns, F2 &ya, F2 &yb) const {
+        ya = mul2(k0[i], a);
+        yb = mul2(k2[i], b);
+        if (turns) {
+            ya = fma2(k1[i], HALF ? b : swap2(a), ya);
+            yb = fma2(k3[i], HALF ? a : swap2(b), yb);
+        }
+    }
+};
+
+// Sum over a group of `lanes` lanes; whole warps.
+QSA_DEVICE float lanes_sum(float x, int lanes) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        if (o < lanes) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// The rows of a group in order: items it, it + stride, ..., rows 0 .. hpg - 1 of each.
+struct Rows {
+    int64_t it, tok;
+    int r, row;   // row in the item, in the token
+    bool live;    // the item is one
+    QSA_DEVICE void locate(int64_t items, int hpg, int n_hg) {
+        live = it < items;
+        r = row = 0;
+        tok = it;
+        if (n_hg > 1) {
+            tok = it / n_hg;
+            row = (int)(it - tok * n_hg) * hpg;
+        }
+    }
+};
+
+// Turns per position of the frequency table, p * freq / 2 pi, once per block.
+QSA_DEVICE void load_table(const double *freq, int rot, double *s_tf) {
+    for (int i = threadIdx.x; i < rot / 2; i += THREADS) s_tf[i] = freq[i] * INV_2PI;
+    __syncthreads();
+}
+
+template <int VEC>
+QSA_DEVICE void table_angles(int64_t p, const double *s_tf, int f0, bool turns, float mscale,
+                             float sign, float (&c)[VEC], float (&s)[VEC]) {
+    double tf[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) tf[e] = turns ? s_tf[f0 + e] : 0.0;
+    angles<VEC>(p, tf, turns, mscale, sign, c, s);
+}
+
 struct NormArgs {
-    const uint16_t *q, *k, *v;
+    const uint16_t *q, *k, *v;   // k and v as if Hq (Hq + Hkv) rows lay before them
     int64_t qs, ks, vs;          // elements between tokens
-    uint16_t *qo, *ko, *vo;
+    uint16_t *qo, *ko, *vo;      // the same
     const float *qw, *kw;        // [D] or nullptr (no norm)
     const int64_t *slot;         // [B, T] cache rows, or nullptr (row = token)
     int64_t L;                   // cache rows per sequence
@@ -251,87 +423,145 @@ struct NormArgs {
     void *status;
 };
 
+// What one thread's ring holds of a row.
+template <int VEC>
+constexpr int norm_line() { return 2 * VEC * 2; }
+constexpr int NORM_STAGES = 8, NORM_CTAS = 2;
+
 template <int VEC, bool HALF>
-__global__ void __launch_bounds__(THREADS) norm_rope_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(THREADS, NORM_CTAS) norm_rope_kernel(const NormArgs a) {
+    using X = Line<uint16_t, VEC>;
+    constexpr int S = NORM_STAGES, HB = X::BYTES * THREADS;  // bytes of half a stage
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ double s_tf[128];
     const int lane = threadIdx.x % a.lanes;
     const Lane<VEC, HALF> L(lane, a.rot);
-    double tf[VEC];
-    load_turns<VEC>(a.freq, L.f0, L.turns, tf);
-    const int64_t per_block = THREADS / a.lanes;
+    const int64_t per_block = THREADS / a.lanes, stride = gridDim.x * per_block;
     const int64_t items = a.n_tok * a.n_hg;
     const float inv_d = 1.f / (float)a.D;
-    // whole warps stay in the loop (the sums are shuffles); `live` guards the memory
-    const int64_t first = blockIdx.x * per_block;
-    for (int64_t base = first; base < items; base += gridDim.x * per_block) {
-        const int64_t it = base + threadIdx.x / a.lanes;
-        const bool live = it < items;
-        const int64_t tok = live ? it / a.n_hg : 0;
-        const int r0 = live ? (int)(it - tok * a.n_hg) * a.hpg : 0;
-        float c[VEC], s[VEC];
-        angles<VEC>(a.pos.at(tok, a.T), tf, L.turns, a.mscale, 1.f, c, s);
-        int64_t orow = tok;  // row of the key and value outputs, or -1: not written
-        if (a.slot && live) {
-            const int64_t sl = a.slot[tok];
-            orow = sl >= 0 && sl < a.L ? tok / a.T * a.L + sl : -1;
-            if (sl >= a.L && lane == 0) record_status(a.status, QSA_ERR_DEVICE);
+    // whole warps stay in the loop (the sums are shuffles): as long as their first group
+    const int64_t wfirst = blockIdx.x * per_block + (threadIdx.x & ~31) / a.lanes;
+    const int steps = wfirst < items ? (int)((items - wfirst + stride - 1) / stride) * a.hpg : 0;
+    Rows in, out;
+    in.it = blockIdx.x * per_block + threadIdx.x / a.lanes;
+    in.locate(items, a.hpg, a.n_hg);
+    out = in;
+    uint8_t *mine = ring + threadIdx.x * X::BYTES;
+    const uint32_t mine32 = smem_u32(mine);
+    const int kr = a.Hq, vr = a.Hq + a.Hkv;
+    auto from = [&](const Rows &w) {
+        return (w.row < kr ? a.q + w.tok * a.qs : w.row < vr ? a.k + w.tok * a.ks
+                                                             : a.v + w.tok * a.vs) + w.row * a.D;
+    };
+    const uint16_t *x_in = from(in);
+    int fill = 0;  // steps begun
+    auto prefetch = [&]() {
+        if (fill < steps && in.live && in.row < a.rows) {
+            const uint32_t d = mine32 + (uint32_t)(fill % S) * (2 * HB);
+            X::copy(d, x_in + L.da);
+            X::copy(d + HB, x_in + L.db);
         }
-        for (int rr = 0; rr < a.hpg; rr += ROWS) {
-            Raw<uint16_t, VEC> ra[ROWS], rb[ROWS];
-            bool on[ROWS];
+        cp_async_commit();
+        ++fill;
+        ++in.row;
+        x_in += a.D;
+        if (++in.r == a.hpg) {
+            in.it += stride;
+            in.locate(items, a.hpg, a.n_hg);
+            x_in = from(in);
+        } else if (in.row == kr || in.row == vr) {
+            x_in = from(in);
+        }
+    };
 #pragma unroll
-            for (int r = 0; r < ROWS; ++r) {
-                const int row = r0 + rr + r;
-                on[r] = live && rr + r < a.hpg && row < a.rows;
-                if (on[r]) {
-                    const uint16_t *x =
-                        row < a.Hq ? a.q + tok * a.qs + (int64_t)row * a.D
-                        : row < a.Hq + a.Hkv
-                            ? a.k + tok * a.ks + (int64_t)(row - a.Hq) * a.D
-                            : a.v + tok * a.vs + (int64_t)(row - a.Hq - a.Hkv) * a.D;
-                    ra[r].load(x + L.da);
-                    rb[r].load(x + L.db);
+    for (int n = 0; n < S - 1; ++n) prefetch();
+    auto position = [&](const Rows &w) { return w.live ? a.pos.at(w.tok, a.T) : 0; };
+    auto slot = [&](const Rows &w) { return a.slot && w.live ? a.slot[w.tok] : 0; };
+    uint16_t *y = nullptr;
+    auto to = [&](const Rows &w, int64_t orow) {
+        return (w.row < kr ? a.qo + w.tok * ((int64_t)a.Hq * a.D)
+                           : (w.row < vr ? a.ko : a.vo) + orow * ((int64_t)a.Hkv * a.D)) +
+               w.row * a.D;
+    };
+    // the next item's position and slot are read an item ahead
+    int64_t p = position(out), sl = slot(out), orow = 0;
+    load_table(a.freq, a.rot, s_tf);
+    float c[VEC], s[VEC];
+    Turn<VEC, HALF> turn;
+    int of = -1;  // whose weight is in `turn`: 0 queries, 1 keys
+    bool fresh = true;
+    for (int n = 0; n < steps; ++n) {
+        cp_async_wait<S - 2>();
+        if (fresh) {
+            table_angles<VEC>(p, s_tf, L.f0, L.turns, a.mscale, 1.f, c, s);
+            orow = out.tok;  // row of the key and value outputs, or -1: not written
+            if (a.slot) {
+                orow = sl >= 0 && sl < a.L ? (a.n_tok == a.T ? 0 : out.tok / a.T * a.L) + sl : -1;
+                if (sl >= a.L && lane == 0 && out.live)
+                    record_status(a.status, QSA_ERR_DEVICE);
+            }
+            of = -1;
+            Rows w = out;
+            w.it += stride;
+            w.locate(items, a.hpg, a.n_hg);
+            p = position(w);
+            sl = slot(w);
+            y = to(out, orow);
+        }
+        const bool on = out.live && out.row < a.rows, isq = out.row < kr, isv = out.row >= vr;
+        X xa, xb;
+        const uint8_t *src = mine + (n % S) * (2 * HB);
+        xa.fetch(src);
+        xb.fetch(src + HB);
+        const float *w = isq ? a.qw : a.kw;
+        if (on && !isv && of != (isq ? 0 : 1)) {
+            of = isq ? 0 : 1;
+            float wa[VEC], wb[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) wa[e] = wb[e] = 1.f;
+            if (w) {
+                load_weight<VEC>(w, L.da, wa);
+                load_weight<VEC>(w, L.db, wb);
+            }
+            turn.set(c, s, wa, wb, L.turns);
+        }
+        F2 ss = pack2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+            const F2 fa = xa.get(i), fb = xb.get(i);
+            ss = fma2(fa, fa, ss);
+            ss = fma2(fb, fb, ss);
+        }
+        const float mean = lanes_sum(sum2(ss), a.lanes) * inv_d;
+        if (on) {
+            if (!isv) {
+                const float rs = w ? rsqrtf(mean + a.eps) : 1.f;
+                const F2 rs2 = pack2(rs, rs);
+#pragma unroll
+                for (int i = 0; i < VEC / 2; ++i) {
+                    F2 ya, yb;
+                    turn.apply(i, xa.get(i), xb.get(i), L.turns, ya, yb);
+                    xa.set(i, mul2(ya, rs2));
+                    xb.set(i, mul2(yb, rs2));
                 }
             }
-#pragma unroll
-            for (int r = 0; r < ROWS; ++r) {
-                const int row = r0 + rr + r;
-                const bool isq = row < a.Hq, isv = row >= a.Hq + a.Hkv;
-                float fa[VEC], fb[VEC];
-                float ss = 0.f;
-                if (on[r]) {
-                    ra[r].get(fa);
-                    rb[r].get(fb);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) ss += fa[e] * fa[e] + fb[e] * fb[e];
-                }
-                ss = group_sum(ss, a.lanes);
-                if (!on[r]) continue;
-                if (!isv) {
-                    const float *w = isq ? a.qw : a.kw;
-                    if (w) {
-                        const float rs = rsqrtf(ss * inv_d + a.eps);
-                        float wa[VEC], wb[VEC];
-                        load_weight<VEC>(w, L.da, wa);
-                        load_weight<VEC>(w, L.db, wb);
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            fa[e] *= rs * wa[e];
-                            fb[e] *= rs * wb[e];
-                        }
-                    }
-                    rotate<VEC, HALF>(fa, fb, c, s);
-                    ra[r].set(fa);
-                    rb[r].set(fb);
-                }
-                if (!isq && orow < 0) continue;
-                uint16_t *y = isq ? a.qo + (tok * a.Hq + row) * a.D
-                              : !isv ? a.ko + (orow * a.Hkv + row - a.Hq) * a.D
-                                     : a.vo + (orow * a.Hkv + row - a.Hq - a.Hkv) * a.D;
-                ra[r].store(y + L.da);
-                rb[r].store(y + L.db);
+            if (isq || orow >= 0) {
+                xa.store(y + L.da);
+                xb.store(y + L.db);
             }
+        }
+        prefetch();
+        ++out.row;
+        y += a.D;
+        fresh = ++out.r == a.hpg;
+        if (fresh) {
+            out.it += stride;
+            out.locate(items, a.hpg, a.n_hg);
+        } else if (out.row == kr || out.row == vr) {
+            y = to(out, orow);
         }
     }
+    cp_async_wait<0>();
 }
 
 // ------------------------------------------------------------- backward --
@@ -360,9 +590,20 @@ struct GradArgs {
     float *part;         // [blocks, D]
 };
 
-template <int VEC, bool HALF, typename TD, typename TX>
-__global__ void __launch_bounds__(THREADS) norm_rope_grad_kernel(const GradArgs a) {
-    constexpr int RB = 2;  // rows whose loads are issued together
+// Vectors of 4: fp32 gradients fill 16 bytes a lane (with 8 a lane's two loads would each
+// touch half of every sector; 195 -> 176 us at 32K tokens before the ring).
+constexpr int GRAD_VEC = 4, GRAD_STAGES = 6, GRAD_CTAS = 2;
+template <typename TD>
+constexpr int grad_line() { return 2 * GRAD_VEC * ((int)sizeof(TD) + 2); }
+
+template <bool HALF, typename TD, typename TX>
+__global__ void __launch_bounds__(THREADS, GRAD_CTAS) norm_rope_grad_kernel(const GradArgs a) {
+    constexpr int VEC = GRAD_VEC, S = GRAD_STAGES;
+    using G = Line<TD, VEC>;
+    using X = Line<uint16_t, VEC>;
+    constexpr int GB = G::BYTES * THREADS, XB = X::BYTES * THREADS, STAGE = 2 * (GB + XB);
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ double s_tf[128];
     __shared__ float s_dw[THREADS / 32][256];
     const bool isq = (int)blockIdx.x < a.n_blocks_q;
     const Side &sd = a.side[isq ? 0 : 1];
@@ -370,100 +611,157 @@ __global__ void __launch_bounds__(THREADS) norm_rope_grad_kernel(const GradArgs 
     const int n_blk = isq ? a.n_blocks_q : gridDim.x - a.n_blocks_q;
     const int lane = threadIdx.x % a.lanes;
     const Lane<VEC, HALF> L(lane, a.rot);
-    double tf[VEC];
-    load_turns<VEC>(a.freq, L.f0, L.turns, tf);
-    float wa[VEC], wb[VEC], ga[VEC], gb[VEC];
+    float wa[VEC], wb[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) ga[e] = gb[e] = wa[e] = wb[e] = 0.f;
-    if (sd.w) {
+    for (int e = 0; e < VEC; ++e) wa[e] = wb[e] = 0.f;
+    const bool norm = sd.w != nullptr;
+    if (norm) {
         load_weight<VEC>(sd.w, L.da, wa);
         load_weight<VEC>(sd.w, L.db, wb);
     }
-    const int64_t per_block = THREADS / a.lanes;
+    F2 ga[VEC / 2], gb[VEC / 2], w2a[VEC / 2], w2b[VEC / 2];
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+        ga[i] = gb[i] = pack2(0.f, 0.f);
+        w2a[i] = pack2(wa[2 * i], wa[2 * i + 1]);
+        w2b[i] = pack2(wb[2 * i], wb[2 * i + 1]);
+    }
+    const int64_t per_block = THREADS / a.lanes, stride = n_blk * per_block;
     const int64_t items = a.n_tok * sd.n_hg;
     const float inv_d = 1.f / (float)a.D;
-    for (int64_t base = blk * per_block; base < items; base += n_blk * per_block) {
-        const int64_t it = base + threadIdx.x / a.lanes;
-        const bool live = it < items;
-        const int64_t tok = live ? it / sd.n_hg : 0;
-        const int h0 = live ? (int)(it - tok * sd.n_hg) * sd.hpg : 0;
-        float c[VEC], s[VEC];
-        angles<VEC>(a.pos.at(tok, a.T), tf, L.turns, a.mscale, -1.f, c, s);
-        for (int hh = 0; hh < sd.hpg; hh += RB) {
-            Raw<TD, VEC> da[RB], db[RB];
-            Raw<uint16_t, VEC> xa[RB], xb[RB];
-            bool on[RB];
+    const int64_t wfirst = blk * per_block + (threadIdx.x & ~31) / a.lanes;
+    const int steps = wfirst < items ? (int)((items - wfirst + stride - 1) / stride) * sd.hpg : 0;
+    Rows in, out;
+    in.it = blk * per_block + threadIdx.x / a.lanes;
+    in.locate(items, sd.hpg, sd.n_hg);
+    out = in;
+    uint8_t *mg = ring + threadIdx.x * G::BYTES, *mx = ring + 2 * GB + threadIdx.x * X::BYTES;
+    const uint32_t mg32 = smem_u32(mg), mx32 = smem_u32(mx);
+    const int H = sd.H, hpg = sd.hpg, n_hg = sd.n_hg;
+    int fill = 0, fslot = 0;
+    const TD *d_in = static_cast<const TD *>(sd.dy) + (in.tok * H + in.row) * a.D;
+    const uint16_t *x_in = sd.x + in.tok * sd.xs + in.row * a.D;
+    auto prefetch = [&]() {
+        if (fill < steps && in.live && in.row < H) {
+            G::copy(mg32 + fslot, d_in + L.da);
+            G::copy(mg32 + fslot + GB, d_in + L.db);
+            X::copy(mx32 + fslot, x_in + L.da);
+            X::copy(mx32 + fslot + XB, x_in + L.db);
+        }
+        cp_async_commit();
+        ++fill;
+        fslot = fslot == (S - 1) * STAGE ? 0 : fslot + STAGE;
+        ++in.row;
+        d_in += a.D;
+        x_in += a.D;
+        if (++in.r == hpg) {
+            in.it += stride;
+            in.locate(items, hpg, n_hg);
+            d_in = static_cast<const TD *>(sd.dy) + (in.tok * H + in.row) * a.D;
+            x_in = sd.x + in.tok * sd.xs + in.row * a.D;
+        }
+    };
 #pragma unroll
-            for (int r = 0; r < RB; ++r) {
-                const int h = h0 + hh + r;
-                on[r] = live && hh + r < sd.hpg && h < sd.H;
-                if (on[r]) {
-                    const TD *d = static_cast<const TD *>(sd.dy) + (tok * sd.H + h) * a.D;
-                    const uint16_t *x = sd.x + tok * sd.xs + (int64_t)h * a.D;
-                    da[r].load(d + L.da);
-                    db[r].load(d + L.db);
-                    xa[r].load(x + L.da);
-                    xb[r].load(x + L.db);
-                }
-            }
+    for (int n = 0; n < S - 1; ++n) prefetch();
+    auto position = [&](const Rows &w) { return w.live ? a.pos.at(w.tok, a.T) : 0; };
+    int64_t p = position(out);
+    load_table(a.freq, a.rot, s_tf);
+    TX *y = nullptr;
+    int at = 0;
+    Turn<VEC, HALF> turn;
+    bool fresh = true;
+    for (int n = 0; n < steps; ++n) {
+        cp_async_wait<S - 2>();
+        if (fresh) {
+            float c[VEC], s[VEC], one[VEC];
+            table_angles<VEC>(p, s_tf, L.f0, L.turns, a.mscale, -1.f, c, s);
 #pragma unroll
-            for (int r = 0; r < RB; ++r) {
-                const int h = h0 + hh + r;
-                float za[VEC], zb[VEC], fa[VEC], fb[VEC];
-                float ss = 0.f, m = 0.f;
+            for (int e = 0; e < VEC; ++e) one[e] = 1.f;
+            turn.set(c, s, one, one, L.turns);
+            Rows w = out;
+            w.it += stride;
+            w.locate(items, hpg, n_hg);
+            p = position(w);
+            y = static_cast<TX *>(sd.dx) + (out.tok * H + out.row) * a.D;
+        }
+        const bool on = out.live && out.row < H;
+        G da, db;
+        X xa, xb;
+        da.fetch(mg + at);
+        db.fetch(mg + at + GB);
+        xa.fetch(mx + at);
+        xb.fetch(mx + at + XB);
+        F2 za[VEC / 2], zb[VEC / 2];
+        F2 ss = pack2(0.f, 0.f), mm = ss;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) za[e] = zb[e] = fa[e] = fb[e] = 0.f;
-                if (on[r]) {
-                    da[r].get(za);
-                    db[r].get(zb);
-                    rotate<VEC, HALF>(za, zb, c, s);
-                    xa[r].get(fa);
-                    xb[r].get(fb);
-                }
-                if (sd.w) {
+        for (int i = 0; i < VEC / 2; ++i) {
+            turn.apply(i, da.get(i), db.get(i), L.turns, za[i], zb[i]);
+            const F2 fa = xa.get(i), fb = xb.get(i);
+            ss = fma2(fa, fa, ss);
+            ss = fma2(fb, fb, ss);
+            mm = fma2(mul2(za[i], w2a[i]), fa, mm);
+            mm = fma2(mul2(zb[i], w2b[i]), fb, mm);
+        }
+        if (norm) {
+            const float mean = lanes_sum(sum2(ss), a.lanes) * inv_d;
+            const float rs = rsqrtf(mean + a.eps);
+            const float m = lanes_sum(sum2(mm), a.lanes) * rs * inv_d;
+            const F2 rs2 = pack2(rs, rs), m2 = pack2(-m, -m);
+            if (on) {
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        ss += fa[e] * fa[e] + fb[e] * fb[e];
-                        m += za[e] * wa[e] * fa[e] + zb[e] * wb[e] * fb[e];
-                    }
-                    ss = group_sum(ss, a.lanes);
-                    m = group_sum(m, a.lanes);
-                    const float rs = rsqrtf(ss * inv_d + a.eps);
-                    m = m * rs * inv_d;
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const float ha = fa[e] * rs, hb = fb[e] * rs;
-                        ga[e] += za[e] * ha;
-                        gb[e] += zb[e] * hb;
-                        za[e] = rs * (za[e] * wa[e] - ha * m);
-                        zb[e] = rs * (zb[e] * wb[e] - hb * m);
-                    }
-                }
-                if (on[r]) {
-                    Raw<TX, VEC> oa, ob;
-                    oa.set(za);
-                    ob.set(zb);
-                    TX *y = static_cast<TX *>(sd.dx) + (tok * sd.H + h) * a.D;
-                    oa.store(y + L.da);
-                    ob.store(y + L.db);
+                for (int i = 0; i < VEC / 2; ++i) {
+                    const F2 ha = mul2(xa.get(i), rs2), hb = mul2(xb.get(i), rs2);
+                    ga[i] = fma2(za[i], ha, ga[i]);
+                    gb[i] = fma2(zb[i], hb, gb[i]);
+                    za[i] = mul2(rs2, fma2(ha, m2, mul2(za[i], w2a[i])));
+                    zb[i] = mul2(rs2, fma2(hb, m2, mul2(zb[i], w2b[i])));
                 }
             }
         }
+        if (on) {
+            Line<TX, VEC> oa, ob;
+#pragma unroll
+            for (int i = 0; i < VEC / 2; ++i) {
+                oa.set(i, za[i]);
+                ob.set(i, zb[i]);
+            }
+            oa.store(y + L.da);
+            ob.store(y + L.db);
+        }
+        prefetch();
+        at = at == (S - 1) * STAGE ? 0 : at + STAGE;
+        ++out.row;
+        y += a.D;
+        fresh = ++out.r == hpg;
+        if (fresh) {
+            out.it += stride;
+            out.locate(items, hpg, n_hg);
+        }
     }
+    cp_async_wait<0>();
     if (!a.part) return;
     // groups of a warp, then warps, each in a fixed order
     const int warp = threadIdx.x >> 5;
+    float fa[VEC], fb[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+        const float2 u = unpack2(ga[i]), v = unpack2(gb[i]);
+        fa[2 * i] = u.x;
+        fa[2 * i + 1] = u.y;
+        fb[2 * i] = v.x;
+        fb[2 * i + 1] = v.y;
+    }
 #pragma unroll
     for (int e = 0; e < VEC; ++e)
         for (int o = a.lanes; o < 32; o <<= 1) {
-            ga[e] += __shfl_xor_sync(0xffffffffu, ga[e], o);
-            gb[e] += __shfl_xor_sync(0xffffffffu, gb[e], o);
+            fa[e] += __shfl_xor_sync(0xffffffffu, fa[e], o);
+            fb[e] += __shfl_xor_sync(0xffffffffu, fb[e], o);
         }
     if ((threadIdx.x & 31) < a.lanes) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            s_dw[warp][L.da + e] = ga[e];
-            s_dw[warp][L.db + e] = gb[e];
+            s_dw[warp][L.da + e] = fa[e];
+            s_dw[warp][L.db + e] = fb[e];
         }
     }
     __syncthreads();
@@ -522,13 +820,12 @@ int grid_of(int64_t items, int lanes, int num_sms, int per_sm) {
     return (int)(need < cap ? (need > 0 ? need : 1) : cap);
 }
 
-// Blocks of the backward: in proportion to the head counts, at least one each.
+// Blocks of the backward: one wave, in proportion to the head counts, at least one each.
 void grad_grid(int64_t n_tok, int Hq, int Hkv, int D, int num_sms, int *nq, int *nk) {
-    const int lanes_min = D / 16;
-    const int total = num_sms * 4;
+    const int total = num_sms * GRAD_CTAS;
     int64_t k = (int64_t)total * Hkv / (Hq + Hkv);
     if (k < 1) k = 1;
-    const int64_t per_block = THREADS / lanes_min;
+    const int64_t per_block = THREADS / (D / (2 * GRAD_VEC));
     const int64_t most_q = (n_tok * Hq + per_block - 1) / per_block;
     const int64_t most_k = (n_tok * Hkv + per_block - 1) / per_block;
     int64_t q = total - k;
@@ -547,12 +844,23 @@ cudaError_t run_rope(const RopeArgs &a, bool half, int grid, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <int VEC, typename TD, typename TX>
-cudaError_t run_grad(const GradArgs &a, bool half, int grid, cudaStream_t s) {
-    if (half)
-        norm_rope_grad_kernel<VEC, true, TD, TX><<<grid, THREADS, 0, s>>>(a);
-    else
-        norm_rope_grad_kernel<VEC, false, TD, TX><<<grid, THREADS, 0, s>>>(a);
+template <int VEC, bool HALF>
+cudaError_t run_norm(const NormArgs &a, int grid, cudaStream_t s) {
+    constexpr int bytes = norm_line<VEC>() * NORM_STAGES * THREADS;
+    auto kern = norm_rope_kernel<VEC, HALF>;
+    const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), bytes);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, THREADS, bytes, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <bool HALF, typename TD, typename TX>
+cudaError_t run_grad(const GradArgs &a, int grid, cudaStream_t s) {
+    constexpr int bytes = grad_line<TD>() * GRAD_STAGES * THREADS;
+    auto kern = norm_rope_grad_kernel<HALF, TD, TX>;
+    const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), bytes);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, THREADS, bytes, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -587,26 +895,18 @@ cudaError_t launch_norm_rope(const uint16_t *q, int64_t qs, const uint16_t *k, i
     using namespace rope;
     const int vec = pick_vec(rot);
     NormArgs a{};
-    a.q = q; a.k = k; a.v = v; a.qs = qs; a.ks = ks; a.vs = vs; a.qo = qo; a.ko = ko; a.vo = vo;
+    const int64_t kr = (int64_t)Hq * D, vr = (int64_t)(Hq + Hkv) * D;
+    a.q = q; a.k = k - kr; a.v = v - vr; a.qs = qs; a.ks = ks; a.vs = vs;
+    a.qo = qo; a.ko = ko - kr; a.vo = vo - vr;
     a.qw = qw; a.kw = kw; a.slot = slot; a.L = L; a.T = T; a.n_tok = (int64_t)B * T;
     a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.rot = rot; a.lanes = D / (2 * vec);
     a.rows = Hq + Hkv + (v ? Hkv : 0);
     a.hpg = heads_per_item(a.n_tok, a.rows, a.lanes, num_sms);
     a.n_hg = (a.rows + a.hpg - 1) / a.hpg;
     a.eps = eps; a.freq = freq; a.mscale = mscale; a.pos = Pos{pos, pos0}; a.status = status;
-    const int grid = grid_of(a.n_tok * a.n_hg, a.lanes, num_sms, 8);
-    if (vec == 8) {
-        if (half)
-            norm_rope_kernel<8, true><<<grid, THREADS, 0, s>>>(a);
-        else
-            norm_rope_kernel<8, false><<<grid, THREADS, 0, s>>>(a);
-    } else {
-        if (half)
-            norm_rope_kernel<4, true><<<grid, THREADS, 0, s>>>(a);
-        else
-            norm_rope_kernel<4, false><<<grid, THREADS, 0, s>>>(a);
-    }
-    return cudaGetLastError();
+    const int grid = grid_of(a.n_tok * a.n_hg, a.lanes, num_sms, NORM_CTAS);
+    if (vec == 8) return half ? run_norm<8, true>(a, grid, s) : run_norm<8, false>(a, grid, s);
+    return half ? run_norm<4, true>(a, grid, s) : run_norm<4, false>(a, grid, s);
 }
 
 // The grid depends on the device, so the workspace is sized for the largest one.
@@ -625,9 +925,8 @@ cudaError_t launch_norm_rope_grad(const void *d_q, const void *d_k, bool d_fp32,
                                   float *dqw, float *dkw, void *ws, int num_sms,
                                   cudaStream_t s) {
     using namespace rope;
-    const int vec = pick_vec(rot);
     GradArgs a{};
-    a.T = T; a.n_tok = (int64_t)B * T; a.D = D; a.rot = rot; a.lanes = D / (2 * vec);
+    a.T = T; a.n_tok = (int64_t)B * T; a.D = D; a.rot = rot; a.lanes = D / (2 * GRAD_VEC);
     a.eps = eps; a.freq = freq; a.mscale = mscale; a.pos = Pos{pos, pos0};
     const int sms = num_sms < 160 ? num_sms : 160;
     auto side = [&](const void *dy, const uint16_t *x, int64_t xs, void *dx, const float *w,
@@ -643,14 +942,13 @@ cudaError_t launch_norm_rope_grad(const void *d_q, const void *d_k, bool d_fp32,
     a.n_blocks_q = nq;
     a.part = dqw || dkw ? reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kWsHeader)
                         : nullptr;
-    cudaError_t e;
     const int grid = nq + nk;
-#define QSA_GRAD(V_, TD_, TX_) run_grad<V_, TD_, TX_>(a, half, grid, s)
-#define QSA_GRAD_T(V_)                                                              \
-    (d_fp32 ? (dx_fp32 ? QSA_GRAD(V_, float, float) : QSA_GRAD(V_, float, uint16_t)) \
-            : (dx_fp32 ? QSA_GRAD(V_, uint16_t, float) : QSA_GRAD(V_, uint16_t, uint16_t)))
-    e = vec == 8 ? QSA_GRAD_T(8) : QSA_GRAD_T(4);
-#undef QSA_GRAD_T
+#define QSA_GRAD(H_)                                                       \
+    (d_fp32 ? (dx_fp32 ? run_grad<H_, float, float>(a, grid, s)            \
+                       : run_grad<H_, float, uint16_t>(a, grid, s))        \
+            : (dx_fp32 ? run_grad<H_, uint16_t, float>(a, grid, s)         \
+                       : run_grad<H_, uint16_t, uint16_t>(a, grid, s)))
+    const cudaError_t e = half ? QSA_GRAD(true) : QSA_GRAD(false);
 #undef QSA_GRAD
     if (e != cudaSuccess || !a.part) return e;
     return launch_dependent(weight_sum_kernel, dim3(D / 32, 2), dim3(1024), 0, s,
