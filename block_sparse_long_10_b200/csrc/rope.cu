@@ -230,13 +230,14 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const RopeArgs a) {
 
 // ---------------------------------------------------- norm and rotation --
 // Both kernels below stream rows (one head of one token): a group of lanes takes an item
-// (a token's run of rows) and its rows one after the other, so that one set of angles
-// serves all of them.  A row's vectors come through a ring in shared memory that belongs
-// to the thread alone (cp.async, no barrier), STAGES rows deep: registers hold one row,
-// and enough bytes are in flight for HBM whatever the occupancy.  The arithmetic is in
-// packed pairs of fp32: unpacked it took half of the issue slots and the time of the loads.
-// Before, with 4 rows in registers: 84 us for 32K tokens forward (16 + 2 heads of 128),
-// 195 us backward with fp32 gradients.
+// (a token, or a batch of its rows) and its batches of rows one after the other, so that
+// one set of angles serves all of them.  Rows come through a ring in shared memory that
+// belongs to the thread alone (cp.async, no barrier), STAGES batches deep: registers hold
+// one batch, and enough bytes are in flight for HBM whatever the occupancy.  What bounds
+// the kernels beyond that is the issue of instructions: so D is a template argument and
+// the batches are unrolled (offsets are immediates), and the arithmetic is in packed pairs
+// of fp32.  32K tokens, 16 + 2 heads of 128, forward / backward with fp32 gradients: rows
+// from registers 84 / 195 us, a ring of single rows 66 / 164 us, this NORM_US / GRAD_US us.
 
 // Packed fp32 pairs.
 struct F2 {
@@ -367,27 +368,35 @@ struct Turn {
     }
 };
 
-// Sum over a group of `lanes` lanes; whole warps.
-QSA_DEVICE float lanes_sum(float x, int lanes) {
+// Sum over a group of LANES lanes; whole warps.
+template <int LANES>
+QSA_DEVICE float lanes_sum(float x) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        if (o < lanes) x += __shfl_xor_sync(0xffffffffu, x, o);
+    for (int o = LANES / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
 
-// The rows of a group in order: items it, it + stride, ..., rows 0 .. hpg - 1 of each.
-struct Rows {
+// Batches of rows of a group in order: items it, it + stride, ..., batches 0 .. hpb - 1 of
+// each, batch `at` of the token.
+struct Batches {
     int64_t it, tok;
-    int r, row;   // row in the item, in the token
+    int n, at;
     bool live;    // the item is one
-    QSA_DEVICE void locate(int64_t items, int hpg, int n_hg) {
+    QSA_DEVICE void locate(int64_t items, int hpb, int n_hg) {
         live = it < items;
-        r = row = 0;
+        n = at = 0;
         tok = it;
         if (n_hg > 1) {
             tok = it / n_hg;
-            row = (int)(it - tok * n_hg) * hpg;
+            at = (int)(it - tok * n_hg) * hpb;
         }
+    }
+    QSA_DEVICE bool next(int64_t stride, int64_t items, int hpb, int n_hg) {
+        ++at;
+        if (++n < hpb) return false;
+        it += stride;
+        locate(items, hpb, n_hg);
+        return true;
     }
 };
 
@@ -407,15 +416,16 @@ QSA_DEVICE void table_angles(int64_t p, const double *s_tf, int f0, bool turns, 
 }
 
 struct NormArgs {
-    const uint16_t *q, *k, *v;   // k and v as if Hq (Hq + Hkv) rows lay before them
-    int64_t qs, ks, vs;          // elements between tokens
-    uint16_t *qo, *ko, *vo;      // the same
-    const float *qw, *kw;        // [D] or nullptr (no norm)
+    const uint16_t *x[3];        // queries, keys, values
+    int64_t xs[3];               // elements between tokens
+    uint16_t *y[3];
+    const float *w[3];           // [D] or nullptr (no norm)
+    int H[3], first[3];          // rows; first batch of a token
     const int64_t *slot;         // [B, T] cache rows, or nullptr (row = token)
     int64_t L;                   // cache rows per sequence
     int64_t T, n_tok;
-    int Hq, Hkv, D, rot, lanes;
-    int rows, hpg, n_hg;         // head rows of a token (q, k and v), per item, items
+    int rot;
+    int batches, hpb, n_hg;      // batches of a token, per item, items of a token
     float eps;
     const double *freq;
     float mscale;
@@ -423,72 +433,60 @@ struct NormArgs {
     void *status;
 };
 
-// What one thread's ring holds of a row.
-template <int VEC>
-constexpr int norm_line() { return 2 * VEC * 2; }
-constexpr int NORM_STAGES = 8, NORM_CTAS = 2;
+constexpr int NORM_ROWS = 4, NORM_STAGES = 3, NORM_CTAS = 2;  // rows of a batch
 
-template <int VEC, bool HALF>
+template <int D, int VEC, bool HALF>
 __global__ void __launch_bounds__(THREADS, NORM_CTAS) norm_rope_kernel(const NormArgs a) {
     using X = Line<uint16_t, VEC>;
-    constexpr int S = NORM_STAGES, HB = X::BYTES * THREADS;  // bytes of half a stage
+    constexpr int LANES = D / (2 * VEC), RB = NORM_ROWS, S = NORM_STAGES;
+    constexpr int HB = X::BYTES * THREADS, STAGE = 2 * HB * RB;
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ double s_tf[128];
-    const int lane = threadIdx.x % a.lanes;
+    const int lane = threadIdx.x % LANES;
     const Lane<VEC, HALF> L(lane, a.rot);
-    const int64_t per_block = THREADS / a.lanes, stride = gridDim.x * per_block;
+    constexpr int per_block = THREADS / LANES;
+    const int64_t stride = (int64_t)gridDim.x * per_block;
     const int64_t items = a.n_tok * a.n_hg;
-    const float inv_d = 1.f / (float)a.D;
     // whole warps stay in the loop (the sums are shuffles): as long as their first group
-    const int64_t wfirst = blockIdx.x * per_block + (threadIdx.x & ~31) / a.lanes;
-    const int steps = wfirst < items ? (int)((items - wfirst + stride - 1) / stride) * a.hpg : 0;
-    Rows in, out;
-    in.it = blockIdx.x * per_block + threadIdx.x / a.lanes;
-    in.locate(items, a.hpg, a.n_hg);
+    const int64_t wfirst = (int64_t)blockIdx.x * per_block + (threadIdx.x & ~31) / LANES;
+    const int steps = wfirst < items ? (int)((items - wfirst + stride - 1) / stride) * a.hpb : 0;
+    Batches in, out;
+    in.it = (int64_t)blockIdx.x * per_block + threadIdx.x / LANES;
+    in.locate(items, a.hpb, a.n_hg);
     out = in;
     uint8_t *mine = ring + threadIdx.x * X::BYTES;
     const uint32_t mine32 = smem_u32(mine);
-    const int kr = a.Hq, vr = a.Hq + a.Hkv;
-    auto from = [&](const Rows &w) {
-        return (w.row < kr ? a.q + w.tok * a.qs : w.row < vr ? a.k + w.tok * a.ks
-                                                             : a.v + w.tok * a.vs) + w.row * a.D;
-    };
-    const uint16_t *x_in = from(in);
-    int fill = 0;  // steps begun
+    // which tensor a batch is of
+    auto part = [&](int at) { return at < a.first[1] ? 0 : at < a.first[2] ? 1 : 2; };
+    int fill = 0, fslot = 0;
     auto prefetch = [&]() {
-        if (fill < steps && in.live && in.row < a.rows) {
-            const uint32_t d = mine32 + (uint32_t)(fill % S) * (2 * HB);
-            X::copy(d, x_in + L.da);
-            X::copy(d + HB, x_in + L.db);
+        if (fill < steps && in.live && in.at < a.batches) {
+            const int t = part(in.at), r0 = (in.at - a.first[t]) * RB, cnt = a.H[t] - r0;
+            const uint16_t *x = a.x[t] + in.tok * a.xs[t] + r0 * D;
+            const uint32_t d = mine32 + fslot;
+#pragma unroll
+            for (int r = 0; r < RB; ++r)
+                if (r < cnt) {
+                    X::copy(d + r * 2 * HB, x + r * D + L.da);
+                    X::copy(d + r * 2 * HB + HB, x + r * D + L.db);
+                }
         }
         cp_async_commit();
         ++fill;
-        ++in.row;
-        x_in += a.D;
-        if (++in.r == a.hpg) {
-            in.it += stride;
-            in.locate(items, a.hpg, a.n_hg);
-            x_in = from(in);
-        } else if (in.row == kr || in.row == vr) {
-            x_in = from(in);
-        }
+        fslot = fslot == (S - 1) * STAGE ? 0 : fslot + STAGE;
+        in.next(stride, items, a.hpb, a.n_hg);
     };
 #pragma unroll
     for (int n = 0; n < S - 1; ++n) prefetch();
-    auto position = [&](const Rows &w) { return w.live ? a.pos.at(w.tok, a.T) : 0; };
-    auto slot = [&](const Rows &w) { return a.slot && w.live ? a.slot[w.tok] : 0; };
-    uint16_t *y = nullptr;
-    auto to = [&](const Rows &w, int64_t orow) {
-        return (w.row < kr ? a.qo + w.tok * ((int64_t)a.Hq * a.D)
-                           : (w.row < vr ? a.ko : a.vo) + orow * ((int64_t)a.Hkv * a.D)) +
-               w.row * a.D;
-    };
+    auto position = [&](const Batches &w) { return w.live ? a.pos.at(w.tok, a.T) : 0; };
+    auto slot = [&](const Batches &w) { return a.slot && w.live ? a.slot[w.tok] : 0; };
     // the next item's position and slot are read an item ahead
     int64_t p = position(out), sl = slot(out), orow = 0;
     load_table(a.freq, a.rot, s_tf);
     float c[VEC], s[VEC];
     Turn<VEC, HALF> turn;
-    int of = -1;  // whose weight is in `turn`: 0 queries, 1 keys
+    int of = -1;  // whose weight is in `turn`
+    int at = 0;
     bool fresh = true;
     for (int n = 0; n < steps; ++n) {
         cp_async_wait<S - 2>();
@@ -497,69 +495,75 @@ __global__ void __launch_bounds__(THREADS, NORM_CTAS) norm_rope_kernel(const Nor
             orow = out.tok;  // row of the key and value outputs, or -1: not written
             if (a.slot) {
                 orow = sl >= 0 && sl < a.L ? (a.n_tok == a.T ? 0 : out.tok / a.T * a.L) + sl : -1;
-                if (sl >= a.L && lane == 0 && out.live)
-                    record_status(a.status, QSA_ERR_DEVICE);
+                if (sl >= a.L && lane == 0 && out.live) record_status(a.status, QSA_ERR_DEVICE);
             }
             of = -1;
-            Rows w = out;
+            Batches w = out;
             w.it += stride;
-            w.locate(items, a.hpg, a.n_hg);
+            w.locate(items, a.hpb, a.n_hg);
             p = position(w);
             sl = slot(w);
-            y = to(out, orow);
         }
-        const bool on = out.live && out.row < a.rows, isq = out.row < kr, isv = out.row >= vr;
-        X xa, xb;
-        const uint8_t *src = mine + (n % S) * (2 * HB);
-        xa.fetch(src);
-        xb.fetch(src + HB);
-        const float *w = isq ? a.qw : a.kw;
-        if (on && !isv && of != (isq ? 0 : 1)) {
-            of = isq ? 0 : 1;
-            float wa[VEC], wb[VEC];
+        const bool on = out.live && out.at < a.batches;
+        const int t = on ? part(out.at) : 2;
+        const int r0 = on ? (out.at - a.first[t]) * RB : 0;
+        const int cnt = on && (t == 0 || orow >= 0) ? a.H[t] - r0 : 0;  // rows to write
+        X xa[RB], xb[RB];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) wa[e] = wb[e] = 1.f;
-            if (w) {
-                load_weight<VEC>(w, L.da, wa);
-                load_weight<VEC>(w, L.db, wb);
+        for (int r = 0; r < RB; ++r) {
+            xa[r].fetch(mine + at + r * 2 * HB);
+            xb[r].fetch(mine + at + r * 2 * HB + HB);
+        }
+        const float *w = a.w[t];
+        float rs[RB];
+        if (__any_sync(0xffffffffu, w != nullptr)) {
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+                F2 ss = pack2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < VEC / 2; ++i) {
+                    const F2 fa = xa[r].get(i), fb = xb[r].get(i);
+                    ss = fma2(fa, fa, ss);
+                    ss = fma2(fb, fb, ss);
+                }
+                rs[r] = rsqrtf(lanes_sum<LANES>(sum2(ss)) * (1.f / D) + a.eps);
             }
-            turn.set(c, s, wa, wb, L.turns);
         }
-        F2 ss = pack2(0.f, 0.f);
+        if (t != 2) {
+            if (of != t) {
+                of = t;
+                float wa[VEC], wb[VEC];
 #pragma unroll
-        for (int i = 0; i < VEC / 2; ++i) {
-            const F2 fa = xa.get(i), fb = xb.get(i);
-            ss = fma2(fa, fa, ss);
-            ss = fma2(fb, fb, ss);
-        }
-        const float mean = lanes_sum(sum2(ss), a.lanes) * inv_d;
-        if (on) {
-            if (!isv) {
-                const float rs = w ? rsqrtf(mean + a.eps) : 1.f;
-                const F2 rs2 = pack2(rs, rs);
+                for (int e = 0; e < VEC; ++e) wa[e] = wb[e] = 1.f;
+                if (w) {
+                    load_weight<VEC>(w, L.da, wa);
+                    load_weight<VEC>(w, L.db, wb);
+                }
+                turn.set(c, s, wa, wb, L.turns);
+            }
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+                const float f = w ? rs[r] : 1.f;
+                const F2 f2 = pack2(f, f);
 #pragma unroll
                 for (int i = 0; i < VEC / 2; ++i) {
                     F2 ya, yb;
-                    turn.apply(i, xa.get(i), xb.get(i), L.turns, ya, yb);
-                    xa.set(i, mul2(ya, rs2));
-                    xb.set(i, mul2(yb, rs2));
+                    turn.apply(i, xa[r].get(i), xb[r].get(i), L.turns, ya, yb);
+                    xa[r].set(i, mul2(ya, f2));
+                    xb[r].set(i, mul2(yb, f2));
                 }
             }
-            if (isq || orow >= 0) {
-                xa.store(y + L.da);
-                xb.store(y + L.db);
+        }
+        uint16_t *y = a.y[t] + ((t == 0 ? out.tok : orow) * a.H[t] + r0) * D;
+#pragma unroll
+        for (int r = 0; r < RB; ++r)
+            if (r < cnt) {
+                xa[r].store(y + r * D + L.da);
+                xb[r].store(y + r * D + L.db);
             }
-        }
         prefetch();
-        ++out.row;
-        y += a.D;
-        fresh = ++out.r == a.hpg;
-        if (fresh) {
-            out.it += stride;
-            out.locate(items, a.hpg, a.n_hg);
-        } else if (out.row == kr || out.row == vr) {
-            y = to(out, orow);
-        }
+        at = at == (S - 1) * STAGE ? 0 : at + STAGE;
+        fresh = out.next(stride, items, a.hpb, a.n_hg);
     }
     cp_async_wait<0>();
 }
@@ -576,13 +580,13 @@ struct Side {
     int64_t xs;
     void *dx;
     const float *w;
-    int H, hpg, n_hg;
+    int H, batches, hpb, n_hg;
 };
 struct GradArgs {
     Side side[2];        // queries, keys
     int n_blocks_q;      // blocks before this one work on the queries
     int64_t T, n_tok;
-    int D, rot, lanes;
+    int rot;
     float eps;
     const double *freq;
     float mscale;
@@ -591,25 +595,26 @@ struct GradArgs {
 };
 
 // Vectors of 4: fp32 gradients fill 16 bytes a lane (with 8 a lane's two loads would each
-// touch half of every sector; 195 -> 176 us at 32K tokens before the ring).
-constexpr int GRAD_VEC = 4, GRAD_STAGES = 6, GRAD_CTAS = 2;
+// touch half of every sector; 195 -> 176 us before the ring).
+constexpr int GRAD_VEC = 4, GRAD_ROWS = 2, GRAD_STAGES = 4, GRAD_CTAS = 2;
 template <typename TD>
-constexpr int grad_line() { return 2 * GRAD_VEC * ((int)sizeof(TD) + 2); }
+constexpr int grad_stage() { return 2 * GRAD_VEC * ((int)sizeof(TD) + 2) * GRAD_ROWS * THREADS; }
 
-template <bool HALF, typename TD, typename TX>
+template <int D, bool HALF, typename TD, typename TX>
 __global__ void __launch_bounds__(THREADS, GRAD_CTAS) norm_rope_grad_kernel(const GradArgs a) {
-    constexpr int VEC = GRAD_VEC, S = GRAD_STAGES;
+    constexpr int VEC = GRAD_VEC, LANES = D / (2 * VEC), RB = GRAD_ROWS, S = GRAD_STAGES;
     using G = Line<TD, VEC>;
     using X = Line<uint16_t, VEC>;
-    constexpr int GB = G::BYTES * THREADS, XB = X::BYTES * THREADS, STAGE = 2 * (GB + XB);
+    constexpr int GB = G::BYTES * THREADS, XB = X::BYTES * THREADS, ROW = 2 * (GB + XB);
+    constexpr int STAGE = ROW * RB;
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ double s_tf[128];
-    __shared__ float s_dw[THREADS / 32][256];
+    __shared__ float s_dw[THREADS / 32][D];
     const bool isq = (int)blockIdx.x < a.n_blocks_q;
     const Side &sd = a.side[isq ? 0 : 1];
     const int blk = isq ? blockIdx.x : blockIdx.x - a.n_blocks_q;
     const int n_blk = isq ? a.n_blocks_q : gridDim.x - a.n_blocks_q;
-    const int lane = threadIdx.x % a.lanes;
+    const int lane = threadIdx.x % LANES;
     const Lane<VEC, HALF> L(lane, a.rot);
     float wa[VEC], wb[VEC];
 #pragma unroll
@@ -626,47 +631,43 @@ __global__ void __launch_bounds__(THREADS, GRAD_CTAS) norm_rope_grad_kernel(cons
         w2a[i] = pack2(wa[2 * i], wa[2 * i + 1]);
         w2b[i] = pack2(wb[2 * i], wb[2 * i + 1]);
     }
-    const int64_t per_block = THREADS / a.lanes, stride = n_blk * per_block;
-    const int64_t items = a.n_tok * sd.n_hg;
-    const float inv_d = 1.f / (float)a.D;
-    const int64_t wfirst = blk * per_block + (threadIdx.x & ~31) / a.lanes;
-    const int steps = wfirst < items ? (int)((items - wfirst + stride - 1) / stride) * sd.hpg : 0;
-    Rows in, out;
-    in.it = blk * per_block + threadIdx.x / a.lanes;
-    in.locate(items, sd.hpg, sd.n_hg);
+    constexpr int per_block = THREADS / LANES;
+    const int64_t stride = (int64_t)n_blk * per_block;
+    const int H = sd.H, hpb = sd.hpb, n_hg = sd.n_hg;
+    const int64_t items = a.n_tok * n_hg;
+    const int64_t wfirst = (int64_t)blk * per_block + (threadIdx.x & ~31) / LANES;
+    const int steps = wfirst < items ? (int)((items - wfirst + stride - 1) / stride) * hpb : 0;
+    Batches in, out;
+    in.it = (int64_t)blk * per_block + threadIdx.x / LANES;
+    in.locate(items, hpb, n_hg);
     out = in;
     uint8_t *mg = ring + threadIdx.x * G::BYTES, *mx = ring + 2 * GB + threadIdx.x * X::BYTES;
     const uint32_t mg32 = smem_u32(mg), mx32 = smem_u32(mx);
-    const int H = sd.H, hpg = sd.hpg, n_hg = sd.n_hg;
     int fill = 0, fslot = 0;
-    const TD *d_in = static_cast<const TD *>(sd.dy) + (in.tok * H + in.row) * a.D;
-    const uint16_t *x_in = sd.x + in.tok * sd.xs + in.row * a.D;
     auto prefetch = [&]() {
-        if (fill < steps && in.live && in.row < H) {
-            G::copy(mg32 + fslot, d_in + L.da);
-            G::copy(mg32 + fslot + GB, d_in + L.db);
-            X::copy(mx32 + fslot, x_in + L.da);
-            X::copy(mx32 + fslot + XB, x_in + L.db);
+        if (fill < steps && in.live) {
+            const int r0 = in.at * RB, cnt = H - r0;
+            const TD *d = static_cast<const TD *>(sd.dy) + (in.tok * H + r0) * D;
+            const uint16_t *x = sd.x + in.tok * sd.xs + r0 * D;
+#pragma unroll
+            for (int r = 0; r < RB; ++r)
+                if (r < cnt) {
+                    G::copy(mg32 + fslot + r * ROW, d + r * D + L.da);
+                    G::copy(mg32 + fslot + r * ROW + GB, d + r * D + L.db);
+                    X::copy(mx32 + fslot + r * ROW, x + r * D + L.da);
+                    X::copy(mx32 + fslot + r * ROW + XB, x + r * D + L.db);
+                }
         }
         cp_async_commit();
         ++fill;
         fslot = fslot == (S - 1) * STAGE ? 0 : fslot + STAGE;
-        ++in.row;
-        d_in += a.D;
-        x_in += a.D;
-        if (++in.r == hpg) {
-            in.it += stride;
-            in.locate(items, hpg, n_hg);
-            d_in = static_cast<const TD *>(sd.dy) + (in.tok * H + in.row) * a.D;
-            x_in = sd.x + in.tok * sd.xs + in.row * a.D;
-        }
+        in.next(stride, items, hpb, n_hg);
     };
 #pragma unroll
     for (int n = 0; n < S - 1; ++n) prefetch();
-    auto position = [&](const Rows &w) { return w.live ? a.pos.at(w.tok, a.T) : 0; };
+    auto position = [&](const Batches &w) { return w.live ? a.pos.at(w.tok, a.T) : 0; };
     int64_t p = position(out);
     load_table(a.freq, a.rot, s_tf);
-    TX *y = nullptr;
     int at = 0;
     Turn<VEC, HALF> turn;
     bool fresh = true;
@@ -678,65 +679,74 @@ __global__ void __launch_bounds__(THREADS, GRAD_CTAS) norm_rope_grad_kernel(cons
 #pragma unroll
             for (int e = 0; e < VEC; ++e) one[e] = 1.f;
             turn.set(c, s, one, one, L.turns);
-            Rows w = out;
+            Batches w = out;
             w.it += stride;
-            w.locate(items, hpg, n_hg);
+            w.locate(items, hpb, n_hg);
             p = position(w);
-            y = static_cast<TX *>(sd.dx) + (out.tok * H + out.row) * a.D;
         }
-        const bool on = out.live && out.row < H;
-        G da, db;
-        X xa, xb;
-        da.fetch(mg + at);
-        db.fetch(mg + at + GB);
-        xa.fetch(mx + at);
-        xb.fetch(mx + at + XB);
-        F2 za[VEC / 2], zb[VEC / 2];
-        F2 ss = pack2(0.f, 0.f), mm = ss;
+        const int r0 = out.at * RB, cnt = out.live ? H - r0 : 0;
+        F2 za[RB][VEC / 2], zb[RB][VEC / 2];
+        X xa[RB], xb[RB];
+        float ss[RB], mm[RB];
 #pragma unroll
-        for (int i = 0; i < VEC / 2; ++i) {
-            turn.apply(i, da.get(i), db.get(i), L.turns, za[i], zb[i]);
-            const F2 fa = xa.get(i), fb = xb.get(i);
-            ss = fma2(fa, fa, ss);
-            ss = fma2(fb, fb, ss);
-            mm = fma2(mul2(za[i], w2a[i]), fa, mm);
-            mm = fma2(mul2(zb[i], w2b[i]), fb, mm);
+        for (int r = 0; r < RB; ++r) {
+            G da, db;
+            da.fetch(mg + at + r * ROW);
+            db.fetch(mg + at + r * ROW + GB);
+            xa[r].fetch(mx + at + r * ROW);
+            xb[r].fetch(mx + at + r * ROW + XB);
+            F2 s2 = pack2(0.f, 0.f), m2 = s2;
+#pragma unroll
+            for (int i = 0; i < VEC / 2; ++i) {
+                turn.apply(i, da.get(i), db.get(i), L.turns, za[r][i], zb[r][i]);
+                const F2 fa = xa[r].get(i), fb = xb[r].get(i);
+                s2 = fma2(fa, fa, s2);
+                s2 = fma2(fb, fb, s2);
+                m2 = fma2(mul2(za[r][i], w2a[i]), fa, m2);
+                m2 = fma2(mul2(zb[r][i], w2b[i]), fb, m2);
+            }
+            ss[r] = sum2(s2);
+            mm[r] = sum2(m2);
         }
         if (norm) {
-            const float mean = lanes_sum(sum2(ss), a.lanes) * inv_d;
-            const float rs = rsqrtf(mean + a.eps);
-            const float m = lanes_sum(sum2(mm), a.lanes) * rs * inv_d;
-            const F2 rs2 = pack2(rs, rs), m2 = pack2(-m, -m);
-            if (on) {
 #pragma unroll
-                for (int i = 0; i < VEC / 2; ++i) {
-                    const F2 ha = mul2(xa.get(i), rs2), hb = mul2(xb.get(i), rs2);
-                    ga[i] = fma2(za[i], ha, ga[i]);
-                    gb[i] = fma2(zb[i], hb, gb[i]);
-                    za[i] = mul2(rs2, fma2(ha, m2, mul2(za[i], w2a[i])));
-                    zb[i] = mul2(rs2, fma2(hb, m2, mul2(zb[i], w2b[i])));
+            for (int r = 0; r < RB; ++r) {
+                ss[r] = lanes_sum<LANES>(ss[r]);
+                mm[r] = lanes_sum<LANES>(mm[r]);
+            }
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+                const float rs = rsqrtf(ss[r] * (1.f / D) + a.eps);
+                const float m = mm[r] * rs * (1.f / D);
+                const F2 rs2 = pack2(rs, rs), m2 = pack2(-m, -m);
+                if (r < cnt) {
+#pragma unroll
+                    for (int i = 0; i < VEC / 2; ++i) {
+                        const F2 ha = mul2(xa[r].get(i), rs2), hb = mul2(xb[r].get(i), rs2);
+                        ga[i] = fma2(za[r][i], ha, ga[i]);
+                        gb[i] = fma2(zb[r][i], hb, gb[i]);
+                        za[r][i] = mul2(rs2, fma2(ha, m2, mul2(za[r][i], w2a[i])));
+                        zb[r][i] = mul2(rs2, fma2(hb, m2, mul2(zb[r][i], w2b[i])));
+                    }
                 }
             }
         }
-        if (on) {
-            Line<TX, VEC> oa, ob;
+        TX *y = static_cast<TX *>(sd.dx) + (out.tok * H + r0) * D;
 #pragma unroll
-            for (int i = 0; i < VEC / 2; ++i) {
-                oa.set(i, za[i]);
-                ob.set(i, zb[i]);
+        for (int r = 0; r < RB; ++r)
+            if (r < cnt) {
+                Line<TX, VEC> oa, ob;
+#pragma unroll
+                for (int i = 0; i < VEC / 2; ++i) {
+                    oa.set(i, za[r][i]);
+                    ob.set(i, zb[r][i]);
+                }
+                oa.store(y + r * D + L.da);
+                ob.store(y + r * D + L.db);
             }
-            oa.store(y + L.da);
-            ob.store(y + L.db);
-        }
         prefetch();
         at = at == (S - 1) * STAGE ? 0 : at + STAGE;
-        ++out.row;
-        y += a.D;
-        fresh = ++out.r == hpg;
-        if (fresh) {
-            out.it += stride;
-            out.locate(items, hpg, n_hg);
-        }
+        fresh = out.next(stride, items, hpb, n_hg);
     }
     cp_async_wait<0>();
     if (!a.part) return;
@@ -753,11 +763,11 @@ __global__ void __launch_bounds__(THREADS, GRAD_CTAS) norm_rope_grad_kernel(cons
     }
 #pragma unroll
     for (int e = 0; e < VEC; ++e)
-        for (int o = a.lanes; o < 32; o <<= 1) {
+        for (int o = LANES; o < 32; o <<= 1) {
             fa[e] += __shfl_xor_sync(0xffffffffu, fa[e], o);
             fb[e] += __shfl_xor_sync(0xffffffffu, fb[e], o);
         }
-    if ((threadIdx.x & 31) < a.lanes) {
+    if ((threadIdx.x & 31) < LANES) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             s_dw[warp][L.da + e] = fa[e];
@@ -765,11 +775,11 @@ __global__ void __launch_bounds__(THREADS, GRAD_CTAS) norm_rope_grad_kernel(cons
         }
     }
     __syncthreads();
-    for (int d = threadIdx.x; d < a.D; d += THREADS) {
+    for (int d = threadIdx.x; d < D; d += THREADS) {
         float t = 0.f;
 #pragma unroll
         for (int w = 0; w < THREADS / 32; ++w) t += s_dw[w][d];
-        a.part[(int64_t)blockIdx.x * a.D + d] = t;
+        a.part[(int64_t)blockIdx.x * D + d] = t;
     }
 }
 
@@ -802,15 +812,19 @@ __global__ void __launch_bounds__(1024)
 // (rot a multiple of 16), else 8-byte ones; fp32 rows always take 16 bytes.
 int pick_vec(int rot) { return rot % 16 == 0 ? 8 : 4; }
 
-// Heads per item: all of a token's rows share one set of angles, but a small batch
-// is spread over more lanes first.  The rotation of a token's `rows` rows costs
-// about as much as its angles at 4 rows, so items are cut to 4 rows only while the
-// GPU has room for them, and to 1 when even those leave SMs idle.
+// Heads per item of the plain rotation: all of a token's rows share one set of angles, but
+// a small batch is spread over more lanes first.
 int heads_per_item(int64_t n_tok, int rows, int lanes, int num_sms) {
     const int64_t want = (int64_t)num_sms * 1024 / lanes;  // groups that fill the GPU
     int hpg = rows;
     while (hpg > 1 && n_tok * ((rows + hpg - 1) / hpg) < want) hpg = (hpg + 1) / 2;
     return hpg;
+}
+
+// Batches of rows per item: a token's batches share one set of angles, unless there are too
+// few tokens for one wave of groups (512 threads an SM).
+int batches_per_item(int64_t n_tok, int batches, int lanes, int num_sms) {
+    return n_tok * lanes >= (int64_t)num_sms * 512 ? batches : 1;
 }
 
 int grid_of(int64_t items, int lanes, int num_sms, int per_sm) {
@@ -844,24 +858,46 @@ cudaError_t run_rope(const RopeArgs &a, bool half, int grid, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <int VEC, bool HALF>
+template <int D, int VEC, bool HALF>
 cudaError_t run_norm(const NormArgs &a, int grid, cudaStream_t s) {
-    constexpr int bytes = norm_line<VEC>() * NORM_STAGES * THREADS;
-    auto kern = norm_rope_kernel<VEC, HALF>;
+    constexpr int bytes = 2 * VEC * 2 * NORM_ROWS * NORM_STAGES * THREADS;
+    auto kern = norm_rope_kernel<D, VEC, HALF>;
     const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), bytes);
     if (e != cudaSuccess) return e;
     kern<<<grid, THREADS, bytes, s>>>(a);
     return cudaGetLastError();
 }
 
-template <bool HALF, typename TD, typename TX>
+template <int D>
+cudaError_t run_norm(const NormArgs &a, int vec, bool half, int grid, cudaStream_t s) {
+    if (vec == 8) return half ? run_norm<D, 8, true>(a, grid, s) : run_norm<D, 8, false>(a, grid, s);
+    return half ? run_norm<D, 4, true>(a, grid, s) : run_norm<D, 4, false>(a, grid, s);
+}
+
+template <int D, bool HALF, typename TD, typename TX>
 cudaError_t run_grad(const GradArgs &a, int grid, cudaStream_t s) {
-    constexpr int bytes = grad_line<TD>() * GRAD_STAGES * THREADS;
-    auto kern = norm_rope_grad_kernel<HALF, TD, TX>;
+    constexpr int bytes = grad_stage<TD>() * GRAD_STAGES;
+    auto kern = norm_rope_grad_kernel<D, HALF, TD, TX>;
     const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), bytes);
     if (e != cudaSuccess) return e;
     kern<<<grid, THREADS, bytes, s>>>(a);
     return cudaGetLastError();
+}
+
+template <int D, bool HALF>
+cudaError_t run_grad(const GradArgs &a, bool d_fp32, bool dx_fp32, int grid, cudaStream_t s) {
+    if (d_fp32)
+        return dx_fp32 ? run_grad<D, HALF, float, float>(a, grid, s)
+                       : run_grad<D, HALF, float, uint16_t>(a, grid, s);
+    return dx_fp32 ? run_grad<D, HALF, uint16_t, float>(a, grid, s)
+                   : run_grad<D, HALF, uint16_t, uint16_t>(a, grid, s);
+}
+
+template <int D>
+cudaError_t run_grad(const GradArgs &a, bool half, bool d_fp32, bool dx_fp32, int grid,
+                     cudaStream_t s) {
+    return half ? run_grad<D, true>(a, d_fp32, dx_fp32, grid, s)
+                : run_grad<D, false>(a, d_fp32, dx_fp32, grid, s);
 }
 
 }  // namespace rope
@@ -893,20 +929,26 @@ cudaError_t launch_norm_rope(const uint16_t *q, int64_t qs, const uint16_t *k, i
                              uint16_t *vo, const int64_t *slot, int64_t L, void *status,
                              int num_sms, cudaStream_t s) {
     using namespace rope;
-    const int vec = pick_vec(rot);
+    const int vec = pick_vec(rot), lanes = D / (2 * vec);
     NormArgs a{};
-    const int64_t kr = (int64_t)Hq * D, vr = (int64_t)(Hq + Hkv) * D;
-    a.q = q; a.k = k - kr; a.v = v - vr; a.qs = qs; a.ks = ks; a.vs = vs;
-    a.qo = qo; a.ko = ko - kr; a.vo = vo - vr;
-    a.qw = qw; a.kw = kw; a.slot = slot; a.L = L; a.T = T; a.n_tok = (int64_t)B * T;
-    a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.rot = rot; a.lanes = D / (2 * vec);
-    a.rows = Hq + Hkv + (v ? Hkv : 0);
-    a.hpg = heads_per_item(a.n_tok, a.rows, a.lanes, num_sms);
-    a.n_hg = (a.rows + a.hpg - 1) / a.hpg;
+    a.x[0] = q; a.x[1] = k; a.x[2] = v;
+    a.xs[0] = qs; a.xs[1] = ks; a.xs[2] = vs;
+    a.y[0] = qo; a.y[1] = ko; a.y[2] = vo;
+    a.w[0] = qw; a.w[1] = kw;
+    a.H[0] = Hq; a.H[1] = a.H[2] = Hkv;
+    const int bk = (Hkv + NORM_ROWS - 1) / NORM_ROWS;
+    a.first[1] = (Hq + NORM_ROWS - 1) / NORM_ROWS;
+    a.first[2] = a.first[1] + bk;
+    a.batches = a.first[2] + (v ? bk : 0);
+    a.slot = slot; a.L = L; a.T = T; a.n_tok = (int64_t)B * T; a.rot = rot;
+    a.hpb = batches_per_item(a.n_tok, a.batches, lanes, num_sms);
+    a.n_hg = a.batches / a.hpb;
     a.eps = eps; a.freq = freq; a.mscale = mscale; a.pos = Pos{pos, pos0}; a.status = status;
-    const int grid = grid_of(a.n_tok * a.n_hg, a.lanes, num_sms, NORM_CTAS);
-    if (vec == 8) return half ? run_norm<8, true>(a, grid, s) : run_norm<8, false>(a, grid, s);
-    return half ? run_norm<4, true>(a, grid, s) : run_norm<4, false>(a, grid, s);
+    const int grid = grid_of(a.n_tok * a.n_hg, lanes, num_sms, NORM_CTAS);
+    return D == 32   ? run_norm<32>(a, vec, half, grid, s)
+           : D == 64 ? run_norm<64>(a, vec, half, grid, s)
+           : D == 128 ? run_norm<128>(a, vec, half, grid, s)
+                      : run_norm<256>(a, vec, half, grid, s);
 }
 
 // The grid depends on the device, so the workspace is sized for the largest one.
@@ -925,15 +967,16 @@ cudaError_t launch_norm_rope_grad(const void *d_q, const void *d_k, bool d_fp32,
                                   float *dqw, float *dkw, void *ws, int num_sms,
                                   cudaStream_t s) {
     using namespace rope;
+    const int lanes = D / (2 * GRAD_VEC);
     GradArgs a{};
-    a.T = T; a.n_tok = (int64_t)B * T; a.D = D; a.rot = rot; a.lanes = D / (2 * GRAD_VEC);
+    a.T = T; a.n_tok = (int64_t)B * T; a.rot = rot;
     a.eps = eps; a.freq = freq; a.mscale = mscale; a.pos = Pos{pos, pos0};
     const int sms = num_sms < 160 ? num_sms : 160;
     auto side = [&](const void *dy, const uint16_t *x, int64_t xs, void *dx, const float *w,
                     int H) {
-        Side d{dy, x, xs, dx, w, H, heads_per_item(a.n_tok, H, a.lanes, sms), 0};
-        d.n_hg = (H + d.hpg - 1) / d.hpg;
-        return d;
+        const int n = (H + GRAD_ROWS - 1) / GRAD_ROWS;
+        const int hpb = batches_per_item(a.n_tok, n, lanes, sms);
+        return Side{dy, x, xs, dx, w, H, n, hpb, n / hpb};
     };
     a.side[0] = side(d_q, q, qs, dq, qw, Hq);
     a.side[1] = side(d_k, k, ks, dk, kw, Hkv);
@@ -943,13 +986,10 @@ cudaError_t launch_norm_rope_grad(const void *d_q, const void *d_k, bool d_fp32,
     a.part = dqw || dkw ? reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kWsHeader)
                         : nullptr;
     const int grid = nq + nk;
-#define QSA_GRAD(H_)                                                       \
-    (d_fp32 ? (dx_fp32 ? run_grad<H_, float, float>(a, grid, s)            \
-                       : run_grad<H_, float, uint16_t>(a, grid, s))        \
-            : (dx_fp32 ? run_grad<H_, uint16_t, float>(a, grid, s)         \
-                       : run_grad<H_, uint16_t, uint16_t>(a, grid, s)))
-    const cudaError_t e = half ? QSA_GRAD(true) : QSA_GRAD(false);
-#undef QSA_GRAD
+    const cudaError_t e = D == 32    ? run_grad<32>(a, half, d_fp32, dx_fp32, grid, s)
+                          : D == 64  ? run_grad<64>(a, half, d_fp32, dx_fp32, grid, s)
+                          : D == 128 ? run_grad<128>(a, half, d_fp32, dx_fp32, grid, s)
+                                     : run_grad<256>(a, half, d_fp32, dx_fp32, grid, s);
     if (e != cudaSuccess || !a.part) return e;
     return launch_dependent(weight_sum_kernel, dim3(D / 32, 2), dim3(1024), 0, s,
                             (const float *)a.part, nq, nk, D, dqw, dkw);
