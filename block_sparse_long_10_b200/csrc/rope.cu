@@ -237,7 +237,8 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const RopeArgs a) {
 // the kernels beyond that is the issue of instructions: so D is a template argument and
 // the batches are unrolled (offsets are immediates), and the arithmetic is in packed pairs
 // of fp32.  32K tokens, 16 + 2 heads of 128, forward / backward with fp32 gradients: rows
-// from registers 84 / 195 us, a ring of single rows 66 / 164 us, this NORM_US / GRAD_US us.
+// from registers 84 / 195 us, a ring of single rows 66 / 164 us, this 61 / 134 us (5.5 and
+// 5.6 TB/s of a copy's 6.5).
 
 // Packed fp32 pairs.
 struct F2 {
@@ -821,10 +822,12 @@ int heads_per_item(int64_t n_tok, int rows, int lanes, int num_sms) {
     return hpg;
 }
 
-// Batches of rows per item: a token's batches share one set of angles, unless there are too
-// few tokens for one wave of groups (512 threads an SM).
+// Batches of rows per item: three, which share one set of angles, or one where there are
+// too few tokens for one wave of groups (512 threads an SM).  Whole tokens leave the last
+// wave half empty: at 32K tokens of 6 batches 65 us with 6, 61 with 3, 65 with 2 (more
+// angles); backward of 8 batches 143 us with 8, 138 with 4, 134 with 3.
 int batches_per_item(int64_t n_tok, int batches, int lanes, int num_sms) {
-    return n_tok * lanes >= (int64_t)num_sms * 512 ? batches : 1;
+    return n_tok * lanes < (int64_t)num_sms * 512 ? 1 : batches < 3 ? batches : 3;
 }
 
 int grid_of(int64_t items, int lanes, int num_sms, int per_sm) {
@@ -942,7 +945,7 @@ cudaError_t launch_norm_rope(const uint16_t *q, int64_t qs, const uint16_t *k, i
     a.batches = a.first[2] + (v ? bk : 0);
     a.slot = slot; a.L = L; a.T = T; a.n_tok = (int64_t)B * T; a.rot = rot;
     a.hpb = batches_per_item(a.n_tok, a.batches, lanes, num_sms);
-    a.n_hg = a.batches / a.hpb;
+    a.n_hg = (a.batches + a.hpb - 1) / a.hpb;
     a.eps = eps; a.freq = freq; a.mscale = mscale; a.pos = Pos{pos, pos0}; a.status = status;
     const int grid = grid_of(a.n_tok * a.n_hg, lanes, num_sms, NORM_CTAS);
     return D == 32   ? run_norm<32>(a, vec, half, grid, s)
@@ -976,7 +979,7 @@ cudaError_t launch_norm_rope_grad(const void *d_q, const void *d_k, bool d_fp32,
                     int H) {
         const int n = (H + GRAD_ROWS - 1) / GRAD_ROWS;
         const int hpb = batches_per_item(a.n_tok, n, lanes, sms);
-        return Side{dy, x, xs, dx, w, H, n, hpb, n / hpb};
+        return Side{dy, x, xs, dx, w, H, n, hpb, (n + hpb - 1) / hpb};
     };
     a.side[0] = side(d_q, q, qs, dq, qw, Hq);
     a.side[1] = side(d_k, k, ks, dk, kw, Hkv);

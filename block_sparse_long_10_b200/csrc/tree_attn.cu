@@ -116,14 +116,20 @@ struct Seg {
     bool begins, ends; // the unit's first (last) tile is in it
 };
 
-// The segments of this CTA, in order.  Each thread that asks walks by itself.
+// The segments of this CTA, in order.  Each thread that asks walks by itself.  A unit counts
+// START tiles more than it has, before its first: a CTA that goes on to another unit drains
+// its pipeline, stores a part and loads queries, the time of about START tiles (without
+// them such CTAs were the last by 8 us of 77, at 8 drafts over 32 prefixes of 8K to 16K).
+constexpr int START = 5;
 template <int NT>
 struct Walk {
     int64_t pos, hi, b, b0;  // b0: flat index of sequence b's first tile
 
-    QSA_DEVICE static int64_t tiles(const Seq &s) { return (s.P + KT - 1) / KT; }
+    QSA_DEVICE static int64_t tiles(const Seq &s) {
+        return s.P > 0 ? (s.P + KT - 1) / KT + START : 0;
+    }
     QSA_DEVICE static int units(const Args &a, const Seq &s) {
-        return (s.n * a.G + 128 * NT - 1) / (128 * NT);
+        return ((s.n << a.lg) + 128 * NT - 1) / (128 * NT);
     }
     QSA_DEVICE static int64_t weight(const Args &a, int64_t b) {
         const Seq s = a.lens.at(b);
@@ -131,17 +137,22 @@ struct Walk {
     }
     // Whole warps; false: nothing for this CTA.
     QSA_DEVICE bool start(const Args &a, int lane) {
-        int64_t total = 0;
-        for (int64_t i = 0; i < a.B; i += 32) total += i + lane < a.B ? weight(a, i + lane) : 0;
+        int64_t total = 0, w0 = 0;
+        for (int64_t i = 0; i < a.B; i += 32) {
+            const int64_t w = i + lane < a.B ? weight(a, i + lane) : 0;
+            if (i == 0) w0 = w;
+            total += w;
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        // no CTA without tiles between two of one unit: the merge reads every slot
         const int64_t ctas = total < gridDim.x ? total : gridDim.x;
         if (blockIdx.x >= ctas) return false;
         pos = total * blockIdx.x / ctas;
         hi = total * (blockIdx.x + 1) / ctas;
         b0 = 0;
         for (int64_t i = 0;; i += 32) {
-            const int64_t w = i + lane < a.B ? weight(a, i + lane) : 0;
+            const int64_t w = i == 0 ? w0 : i + lane < a.B ? weight(a, i + lane) : 0;
             int64_t end = w;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -159,28 +170,32 @@ struct Walk {
         }
     }
     QSA_DEVICE bool next(const Args &a, Seg &s) {
-        if (pos >= hi) return false;
-        Seq sq = a.lens.at(b);
-        int64_t w = tiles(sq) * units(a, sq) * a.Hkv;
-        while (pos >= b0 + w) {
-            b0 += w;
-            sq = a.lens.at(++b);
-            w = tiles(sq) * units(a, sq) * a.Hkv;
+        while (pos < hi) {
+            Seq sq = a.lens.at(b);
+            int64_t nt = tiles(sq), w = nt * units(a, sq) * a.Hkv;
+            while (pos >= b0 + w) {
+                b0 += w;
+                sq = a.lens.at(++b);
+                nt = tiles(sq);
+                w = nt * units(a, sq) * a.Hkv;
+            }
+            const int64_t u = (pos - b0) / nt;
+            const int qn = units(a, sq);
+            const int64_t t = pos - b0 - u * nt, n = nt - t < hi - pos ? nt - t : hi - pos;
+            pos += n;
+            if (t + n <= START) continue;  // only tiles that stand for the start
+            s.b = b;
+            s.P = sq.P;
+            s.nd = sq.n;
+            s.g = (int)(u / qn);
+            s.qt = (int)(u - (int64_t)s.g * qn);
+            s.t0 = t > START ? t - START : 0;
+            s.n = (int)(t + n - START - s.t0);
+            s.begins = s.t0 == 0;
+            s.ends = t + n == nt;
+            return true;
         }
-        const int64_t nt = tiles(sq), u = (pos - b0) / nt;
-        const int qn = units(a, sq);
-        s.b = b;
-        s.P = sq.P;
-        s.nd = sq.n;
-        s.g = (int)(u / qn);
-        s.qt = (int)(u - (int64_t)s.g * qn);
-        s.t0 = pos - b0 - u * nt;
-        const int64_t n = nt - s.t0 < hi - pos ? nt - s.t0 : hi - pos;
-        s.n = (int)n;
-        s.begins = s.t0 == 0;
-        s.ends = s.t0 + n == nt;
-        pos += n;
-        return true;
+        return false;
     }
 };
 
