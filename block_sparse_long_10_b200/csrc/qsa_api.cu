@@ -653,7 +653,7 @@ qsa_status_t qsa_dense_tree_decode(const qsa_bf16_t *q, const qsa_bf16_t *k_cach
 size_t qsa_sparse_tree_decode_workspace_size(int B, int N, int Hq, int D, int r, int budget) {
     if (B < 1 || N < 1 || Hq < 1 || D < 1 || r < 1 || budget < r || budget % r != 0)
         return SIZE_MAX;
-    return qsa::tree_sparse_ws_bytes(B, N, Hq, D, budget / r);
+    return qsa::tree_sparse_ws_bytes(B, N, Hq, D);
 }
 
 qsa_status_t qsa_sparse_tree_decode(const qsa_bf16_t *q, const qsa_bf16_t *k_cache,
@@ -670,7 +670,7 @@ qsa_status_t qsa_sparse_tree_decode(const qsa_bf16_t *q, const qsa_bf16_t *k_cac
     if (st != QSA_OK) return st;
     if (!sel) return QSA_ERR_INVALID_ARG;
     if (r != 4 || budget / r > 1024) return QSA_ERR_UNSUPPORTED_SHAPE;
-    if (!ws || ws_bytes < qsa::tree_sparse_ws_bytes(B, N, Hq, D, budget / r) || !aligned16(ws))
+    if (!ws || ws_bytes < qsa::tree_sparse_ws_bytes(B, N, Hq, D) || !aligned16(ws))
         return QSA_ERR_WORKSPACE;
     int sms = 0;
     st = current_device(&sms);

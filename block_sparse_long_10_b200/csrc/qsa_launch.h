@@ -150,16 +150,16 @@ struct TreePrefix {
     int N;
     const int32_t *sel;                // row (b, i) at b * sel_b + i * sel_n
     int64_t sel_b, sel_n;
-    float *o, *ml;                     // part (row * nsplit + split) * Hq + h
+    float *o, *ml;                     // part (CTA + row) * Hq + h
+    int32_t *first, *last;             // [rows]: first and last CTA of a row
 };
-int tree_sparse_splits(int64_t rows, int kb, int Hkv);
+int tree_sparse_ctas(int num_sms);
 cudaError_t launch_tree_sparse_prefix(const uint16_t *q, const uint16_t *k, const uint16_t *v,
-                                      const TreePrefix &t, int64_t L_max, int kb, int nsplit,
-                                      int B, int Hq, int Hkv, int D, float scale, int num_sms,
-                                      cudaStream_t s);
+                                      const TreePrefix &t, int64_t L_max, int kb, int B, int Hq,
+                                      int Hkv, int D, float scale, int ctas, cudaStream_t s);
 int tree_max_drafts();
 size_t tree_dense_ws_bytes(int B, int N, int Hq, int Hkv, int D);
-size_t tree_sparse_ws_bytes(int B, int N, int Hq, int D, int kb);
+size_t tree_sparse_ws_bytes(int B, int N, int Hq, int D);
 cudaError_t launch_tree_decode(const uint16_t *q, const uint16_t *k, const uint16_t *v,
                                const int32_t *seqlens, const int32_t *n_draft, int64_t L_max,
                                const int32_t *sel, int64_t sel_b, int64_t sel_n, int kb,

@@ -33,7 +33,8 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
 // TREE: a slice of one drafted token's selection over its committed prefix; entry
-// kb - 1 stands for the tokens after the last complete block.
+// kb - 1 stands for the tokens after the last complete block.  All rows' stages, in one
+// row, are cut into equal runs, one per CTA; each row that a run meets leaves a part.
 enum Mode { PREFILL = 0, SPLIT = 1, TREE = 2 };
 
 // Prefill: 2-stage ring, 3 CTAs per SM (12 warps: the gather is latency-bound
@@ -84,6 +85,66 @@ struct Args {
     TreePrefix tree;         // TREE mode
 };
 
+// A CTA's run of stages over all live rows, nst stages each.
+struct TreeRun {
+    int64_t pos, hi, b, b0;  // b0: flat index of sequence b's first stage
+    int64_t P;               // of the current row: committed tokens
+    int i, s0, n, nst;       // draft, first stage, stages
+
+    QSA_DEVICE static int drafts(const TreePrefix &t, int64_t b, int64_t Tk, int64_t &P) {
+        const int64_t S = t.seqlens[b];
+        const int n = t.n_draft ? t.n_draft[b] : t.N;
+        P = S - n;
+        // lengths out of range leave no rows: the merge reports them
+        return n < 0 || n > t.N || S < n || S > Tk ? 0 : n;
+    }
+    // Whole warps; false: nothing for this CTA.
+    QSA_DEVICE bool start(const TreePrefix &t, int B, int64_t Tk, int nst_, int lane) {
+        nst = nst_;
+        int64_t total = 0, skip;
+        for (int64_t j = lane; j < B; j += 32) total += drafts(t, j, Tk, skip);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        total *= nst;
+        const int64_t ctas = total < gridDim.x ? total : gridDim.x;
+        if (blockIdx.x >= ctas) return false;
+        pos = total * blockIdx.x / ctas;
+        hi = total * (blockIdx.x + 1) / ctas;
+        b0 = 0;
+        for (int64_t j = 0;; j += 32) {
+            const int64_t w = j + lane < B ? (int64_t)drafts(t, j + lane, Tk, skip) * nst : 0;
+            int64_t end = w;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, end, o);
+                if (lane >= o) end += y;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, b0 + end > pos);
+            if (past) {
+                const int f = __ffs(past) - 1;
+                b = j + f;
+                b0 += __shfl_sync(0xffffffffu, end - w, f);
+                return true;
+            }
+            b0 += __shfl_sync(0xffffffffu, end, 31);
+        }
+    }
+    QSA_DEVICE bool next(const TreePrefix &t, int64_t Tk) {
+        if (pos >= hi) return false;
+        int64_t w = (int64_t)drafts(t, b, Tk, P) * nst;
+        while (pos >= b0 + w) {
+            b0 += w;
+            w = (int64_t)drafts(t, ++b, Tk, P) * nst;
+        }
+        const int at = (int)(pos - b0);  // N * nst at most
+        i = at / nst;
+        s0 = at - i * nst;
+        n = (int)(hi - pos < nst - s0 ? hi - pos : nst - s0);
+        pos += n;
+        return true;
+    }
+};
+
 template <int D, int G, int HKV, int MODE>
 __global__ void __launch_bounds__(THREADS, Ring<MODE>::CTAS) sparse_attn_kernel(const Args a) {
     griddep_wait();  // the selection (and partial buffers) of the previous kernel
@@ -97,7 +158,10 @@ __global__ void __launch_bounds__(THREADS, Ring<MODE>::CTAS) sparse_attn_kernel(
     const int g = warp / C::WPG, sub = warp % C::WPG;
     const int Hq = HKV * G;
 
-    for (int64_t item = blockIdx.x; item < a.total_items; item += gridDim.x) {
+    TreeRun run;
+    if (MODE == TREE && !run.start(a.tree, a.B, a.Tk, (a.kb + C::NBS - 1) / C::NBS, lane)) return;
+    for (int64_t item = blockIdx.x; MODE == TREE ? run.next(a.tree, a.Tk) : item < a.total_items;
+         item += gridDim.x) {
         // ---- describe the item ------------------------------------------
         int64_t b, row, p;
         int e0, e1;
@@ -111,18 +175,16 @@ __global__ void __launch_bounds__(THREADS, Ring<MODE>::CTAS) sparse_attn_kernel(
             e1 = a.kb;
             qrow = a.q + row * Hq * D;
         } else if (MODE == TREE) {
-            row = item / a.nsplit;
-            b = row / a.tree.N;
-            const int i = (int)(row - b * a.tree.N);
-            const int split = (int)(item - row * a.nsplit);
-            const int64_t S = a.seqlens[b];
-            const int n = a.tree.n_draft ? a.tree.n_draft[b] : a.tree.N;
-            // no such draft, or lengths that the merge reports
-            if (i >= n || n > a.tree.N || S < n || S > a.Tk) continue;
-            p = S - n - 1;
-            e0 = split * a.chunk;
-            e1 = min(e0 + a.chunk, a.kb);
+            b = run.b;
+            row = b * a.tree.N + run.i;
+            p = run.P - 1;
+            e0 = run.s0 * C::NBS;
+            e1 = min(e0 + run.n * C::NBS, a.kb);
             qrow = a.q + row * Hq * D;
+            if (tid == 0) {
+                if (run.s0 == 0) a.tree.first[row] = blockIdx.x;
+                if (e1 == a.kb) a.tree.last[row] = blockIdx.x;
+            }
         } else {
             b = item / a.nsplit;
             row = b;
@@ -327,7 +389,7 @@ __global__ void __launch_bounds__(THREADS, Ring<MODE>::CTAS) sparse_attn_kernel(
                 if (a.lse && d == 0)
                     a.lse[row * Hq + h] = L > 0.f ? (M + __log2f(L)) * LN2 : -INFINITY;
             } else if (MODE == TREE) {
-                const int64_t x = item * Hq + h;
+                const int64_t x = (blockIdx.x + row) * Hq + h;
                 a.tree.o[x * D + d] = O;
                 if (d == 0) {
                     a.tree.ml[x * 2] = M;
@@ -442,27 +504,16 @@ cudaError_t launch_split_decode(const uint16_t *q, const uint16_t *k, const uint
                             (const float *)part, B, Hq, nsplit, o, lse);
 }
 
-// A tree's rows fill the GPU three times over, or each is split until they do; a slice
-// keeps at least two stages.
-int tree_sparse_splits(int64_t rows, int kb, int Hkv) {
-    const int64_t most = (kb + 1) / (2 * sparse_attn_blocks_per_stage(Hkv));
-    int64_t ns = 148 * sat::Ring<sat::TREE>::CTAS / rows;
-    if (ns > most) ns = most;
-    return (int)(ns < 1 ? 1 : ns);
-}
+int tree_sparse_ctas(int num_sms) { return num_sms * sat::Ring<sat::TREE>::CTAS; }
 
 cudaError_t launch_tree_sparse_prefix(const uint16_t *q, const uint16_t *k, const uint16_t *v,
-                                      const TreePrefix &t, int64_t L_max, int kb, int nsplit,
-                                      int B, int Hq, int Hkv, int D, float scale, int num_sms,
-                                      cudaStream_t s) {
+                                      const TreePrefix &t, int64_t L_max, int kb, int B, int Hq,
+                                      int Hkv, int D, float scale, int ctas, cudaStream_t s) {
     sat::Args a{};
     a.q = q; a.k = k; a.v = v; a.seqlens = t.seqlens; a.B = B; a.Tk = L_max; a.Hq = Hq;
-    a.kb = kb + 1; a.nsplit = nsplit; a.chunk = (kb + nsplit) / nsplit;
-    a.scale_log2 = scale * sat::LOG2E; a.tree = t;
-    a.total_items = (int64_t)B * t.N * nsplit;
-    const int64_t slots = (int64_t)num_sms * sat::Ring<sat::TREE>::CTAS;
-    const int64_t grid = a.total_items < slots ? a.total_items : slots;
-    return sat::dispatch<sat::TREE>(a, D, Hq / Hkv, Hkv, (int)grid, s);
+    a.kb = kb + 1; a.scale_log2 = scale * sat::LOG2E; a.tree = t;
+    a.total_items = (int64_t)B * t.N;
+    return sat::dispatch<sat::TREE>(a, D, Hq / Hkv, Hkv, ctas, s);
 }
 
 }  // namespace qsa

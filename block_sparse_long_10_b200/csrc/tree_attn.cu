@@ -56,9 +56,10 @@ struct Args {
     float scale_log2;
     // prefix parts: part x holds O[x * D ..] and (max, sum)[x * 2 ..]
     float *part, *ml;
-    int nsplit;          // sparse: parts (row * nsplit + split) * Hq + h
-    int units, rows;     // dense: units per sequence, rows per unit
-    int32_t *first, *last;  // dense: [B * units] first and last CTA of a unit
+    // Units: dense, `rows` (draft, head) pairs of a KV head, `units` to a (sequence, KV head);
+    // sparse, the heads of a draft.  CTA c leaves unit u's row r in part (c + u) * rows + r.
+    int units, rows;
+    int32_t *first, *last;  // first and last CTA of each unit
     uint16_t *o;
     float *lse;
     void *status;
@@ -705,24 +706,20 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const Args a) {
         }
     }
     griddep_wait();  // the prefix parts
-    int64_t x0 = 0, dx = 0;
+    int64_t x0 = 0;
     int parts = 0;
-    if (SPARSE) {
-        x0 = row * a.nsplit * a.Hq + h;
-        dx = a.Hq;
-        parts = sq.bad ? 0 : a.nsplit;
-    } else if (sq.P > 0) {
-        const int rr = (i << a.lg) + (h & (a.G - 1)), qt = rr / a.rows;
-        const int64_t u = (b * a.Hkv + (h >> a.lg)) * a.units + qt;
+    if (SPARSE ? !sq.bad : sq.P > 0) {
+        // unit and row in it
+        const int rr = SPARSE ? h : (i << a.lg) + (h & (a.G - 1)), qt = rr / a.rows;
+        const int64_t u = SPARSE ? row : (b * a.Hkv + (h >> a.lg)) * a.units + qt;
         const int first = a.first[u];
         x0 = (first + u) * a.rows + (rr - qt * a.rows);
-        dx = a.rows;
         parts = a.last[u] - first + 1;
     }
     float2 ml;
     float4 f[E / 4];
     auto fetch = [&](int s) {
-        const int64_t x = x0 + s * dx;
+        const int64_t x = x0 + (int64_t)s * a.rows;
         ml = *reinterpret_cast<const float2 *>(a.ml + x * 2);
 #pragma unroll
         for (int e = 0; e < E / 4; ++e)
@@ -795,18 +792,22 @@ int unit_rows(int N, int G) {
 }
 int unit_count(int N, int G) { return (N * G + unit_rows(N, G) - 1) / unit_rows(N, G); }
 
-struct DenseWs {
+struct Workspace {
     size_t first, last, part, ml, bytes;
-    DenseWs(int B, int N, int Hkv, int G, int D) {
-        const size_t units = (size_t)B * Hkv * unit_count(N, G);
-        const size_t x = (MAX_CTAS + units) * unit_rows(N, G);
+    Workspace(size_t ctas, size_t units, size_t rows, size_t D) {
         first = kWsHeader;
         last = first + (units * 4 + 255) / 256 * 256;
         part = last + (units * 4 + 255) / 256 * 256;
-        ml = part + x * D * 4;
-        bytes = ml + x * 8;
+        ml = part + (ctas + units) * rows * D * 4;
+        bytes = ml + (ctas + units) * rows * 8;
     }
 };
+Workspace dense_ws(int B, int N, int Hkv, int G, int D) {
+    return Workspace(MAX_CTAS, (size_t)B * Hkv * unit_count(N, G), unit_rows(N, G), D);
+}
+Workspace sparse_ws(int B, int N, int Hq, int D) {
+    return Workspace(tree_sparse_ctas(MAX_CTAS), (size_t)B * N, Hq, D);
+}
 
 template <int D, int NT>
 cudaError_t run_dense(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, int ctas,
@@ -834,13 +835,11 @@ cudaError_t run_merge(const Args &a, cudaStream_t s) {
 int tree_max_drafts() { return tree::MAX_N; }
 
 size_t tree_dense_ws_bytes(int B, int N, int Hq, int Hkv, int D) {
-    return tree::DenseWs(B, N, Hkv, Hq / Hkv, D).bytes;
+    return tree::dense_ws(B, N, Hkv, Hq / Hkv, D).bytes;
 }
 
-// The split depends on the KV heads, which the size does not: the most of any.
-size_t tree_sparse_ws_bytes(int B, int N, int Hq, int D, int kb) {
-    const int64_t rows = (int64_t)B * N;
-    return kWsHeader + (size_t)rows * tree_sparse_splits(rows, kb, 4) * Hq * (D + 2) * sizeof(float);
+size_t tree_sparse_ws_bytes(int B, int N, int Hq, int D) {
+    return tree::sparse_ws(B, N, Hq, D).bytes;
 }
 
 cudaError_t launch_tree_decode(const uint16_t *q, const uint16_t *k, const uint16_t *v,
@@ -855,34 +854,34 @@ cudaError_t launch_tree_decode(const uint16_t *q, const uint16_t *k, const uint1
     a.parent = parent; a.B = B; a.N = N; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv;
     while (1 << a.lg < a.G) ++a.lg;  // 1, 2, 4 or 8 heads to a KV head
     a.scale_log2 = scale * tree::LOG2E; a.o = o; a.lse = lse; a.status = ws;
+    const tree::Workspace x =
+        sel ? tree::sparse_ws(B, N, Hq, D) : tree::dense_ws(B, N, Hkv, a.G, D);
+    a.first = reinterpret_cast<int32_t *>(w + x.first);
+    a.last = reinterpret_cast<int32_t *>(w + x.last);
+    a.part = reinterpret_cast<float *>(w + x.part);
+    a.ml = reinterpret_cast<float *>(w + x.ml);
+    const int sms = num_sms < tree::MAX_CTAS ? num_sms : tree::MAX_CTAS;
     cudaError_t e;
     if (sel) {
-        a.nsplit = tree_sparse_splits((int64_t)B * N, kb, Hkv);
-        a.part = reinterpret_cast<float *>(w + kWsHeader);
-        a.ml = a.part + (int64_t)B * N * a.nsplit * Hq * D;
-        const TreePrefix t{seqlens, n_draft, N, sel, sel_b, sel_n, a.part, a.ml};
-        e = launch_tree_sparse_prefix(q, k, v, t, L_max, kb, a.nsplit, B, Hq, Hkv, D, scale,
-                                      num_sms, s);
+        a.units = 1;
+        a.rows = Hq;
+        const TreePrefix t{seqlens, n_draft, N, sel, sel_b, sel_n, a.part, a.ml, a.first, a.last};
+        e = launch_tree_sparse_prefix(q, k, v, t, L_max, kb, B, Hq, Hkv, D, scale,
+                                      tree_sparse_ctas(sms), s);
     } else {
-        const tree::DenseWs x(B, N, Hkv, a.G, D);
         a.units = tree::unit_count(N, a.G);
         a.rows = tree::unit_rows(N, a.G);
-        a.first = reinterpret_cast<int32_t *>(w + x.first);
-        a.last = reinterpret_cast<int32_t *>(w + x.last);
-        a.part = reinterpret_cast<float *>(w + x.part);
-        a.ml = reinterpret_cast<float *>(w + x.ml);
         CUtensorMap tk, tv;
         if (!tensor_map_cache_bf16(&tk, k, B, L_max, Hkv * D, tree::KT) ||
             !tensor_map_cache_bf16(&tv, v, B, L_max, Hkv * D, tree::KT))
             return cudaErrorInvalidValue;
-        const int ctas = num_sms < tree::MAX_CTAS ? num_sms : tree::MAX_CTAS;
         const bool two = tree::unit_tiles(N, a.G) == 2;
         if (D == 64)
-            e = two ? tree::run_dense<64, 2>(tk, tv, a, ctas, s)
-                    : tree::run_dense<64, 1>(tk, tv, a, ctas, s);
+            e = two ? tree::run_dense<64, 2>(tk, tv, a, sms, s)
+                    : tree::run_dense<64, 1>(tk, tv, a, sms, s);
         else
-            e = two ? tree::run_dense<128, 2>(tk, tv, a, ctas, s)
-                    : tree::run_dense<128, 1>(tk, tv, a, ctas, s);
+            e = two ? tree::run_dense<128, 2>(tk, tv, a, sms, s)
+                    : tree::run_dense<128, 1>(tk, tv, a, sms, s);
     }
     if (e != cudaSuccess) return e;
     if (sel) return D == 64 ? tree::run_merge<64, true>(a, s) : tree::run_merge<128, true>(a, s);
