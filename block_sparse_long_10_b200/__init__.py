@@ -1,9 +1,10 @@
 """Python binding of libqsa, the B200 (sm_100a) Qwen Sparse Attention library.
 
-Thin ctypes layer over the C ABI declared in ``include/qsa.h``: every function
-here has the C entry point's name, checks that its torch tensors have the
-dtype, device and contiguity the ABI requires, and passes their device
-pointers, the sizes and the current CUDA stream through.  All computation
+Thin layer over the C ABI declared in ``include/qsa.h`` (ctypes, and a native
+module for the calls of a decode step): every function here has the C entry
+point's name, checks that its torch tensors have the dtype, device and
+contiguity the ABI requires, and passes their device pointers, the sizes and
+the current CUDA stream through.  All computation
 happens in the library's CUDA kernels; there is no other code path.  If the
 shared library has not been built, every call raises ``QSAError``.
 
@@ -490,84 +491,21 @@ def qsa_index_distill_sparse(q, k, lse, sel, q_idx, w, k_pooled, kl, dq_idx, dw,
 
 # ------------------------------------------ rotary positions, per-head norms --
 
-_LAYOUT = {"half": 0, "interleaved": 1}
 _SCALING = {"none": 0, "linear": 1, "ntk": 2, "by-parts": 3}
-_DTYPE = {torch.bfloat16: 0, torch.float32: 1}
+_ext = None
 
 
-_Tensor = torch.Tensor
-
-
-def _arg(t, dtype, shape, dev, name):
-    """The pointer of a contiguous tensor of this type and shape on device `dev` (None passes).
-    A step of a few microseconds on the GPU passes a dozen tensors: one line tells that all
-    is well, what is wrong is found after it."""
-    if t is None:
-        return None
-    if (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-            and t.get_device() == dev and dev >= 0):
-        return t.data_ptr()
-    _need(t, dtype, name, len(shape))
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
-
-
-def _given(t, name, ndim):
-    """A tensor from whose shape and device the others' follow."""
-    if not isinstance(t, _Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != ndim:
-        raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
-    return t.get_device()
-
-
-def _space(ws, dev):
-    """The pointer of a workspace, whatever its size."""
-    _given(ws, "ws", 1)
-    return _arg(ws, torch.uint8, ws.shape, dev, "ws")
-
-
-def _rows(t, dtype, shape, dev, name):
-    """(pointer, stride) of a [B,T,H,D] tensor whose tokens lie at one stride, heads packed."""
-    if not isinstance(t, _Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.get_device() != dev or dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor on one device with the others, "
-                         f"is on {t.device}")
-    B, T, H, D = shape
-    if t.is_contiguous():
-        return t.data_ptr(), H * D
-    sb, st, sh, sd = t.stride()
-    if T == 1:
-        st = sb if B > 1 else H * D
-    if (D > 1 and sd != 1) or (H > 1 and sh != D) or (B > 1 and T > 0 and sb != T * st):
-        raise ValueError(f"{name}'s tokens must lie at one stride, its heads packed; "
-                         f"strides {t.stride()}")
-    return t.data_ptr(), (max(st, H * D) if B * T <= 1 else st)
-
-
-def _layout(layout):
-    if layout not in _LAYOUT:
-        raise ValueError(f"layout must be one of {sorted(_LAYOUT)}, got {layout!r}")
-    return _LAYOUT[layout]
-
-
-def _call_on(dev, stream, name, *args):
-    """_call with device `dev` current (the library launches on the current device) and its
-    current stream, or `stream`, as the last argument."""
-    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == dev:
-        rc = getattr(_lib or load(), name)(*args, s)
-    else:
-        with torch.cuda.device(dev):
-            rc = getattr(_lib or load(), name)(*args, s)
-    if rc != 0:
-        raise QSAError(rc, name)
+def _native():
+    """The native binding of the calls below (csrc/bind.cpp), loaded once: it makes the checks
+    of the tensors and the call itself, which in Python take longer than the launch."""
+    global _ext
+    load()
+    try:
+        from . import _bind
+    except ImportError as e:
+        raise QSAError(-1, f"the native binding is not built (run __graft_entry__.build()): {e}")
+    _ext = _bind
+    return _ext
 
 
 def qsa_rope_frequencies(base, rot, scaling="none", factor=1.0, orig_len=0.0, beta_fast=32.0,
@@ -584,30 +522,14 @@ def qsa_rope_frequencies(base, rot, scaling="none", factor=1.0, orig_len=0.0, be
     return (freq if device is None else freq.to(device)), mscale.value
 
 
-def _freq(freq, dev):
-    """(pointer, rot) of a frequency table; None: no rotation."""
-    if freq is None:
-        return None, 0
-    _given(freq, "freq", 1)
-    n = freq.numel()
-    return _arg(freq, torch.float64, (n,), dev, "freq"), 2 * n
-
-
 def qsa_rope(x, y, freq, pos=None, pos0=None, layout="half", mscale=1.0, transpose=False,
              stream=None):
     """x [B,T,H,D] bf16 or fp32 -> y (same type; may be x): the first 2 * len(freq) dims of
     each head turned by position * freq; transpose: the gradient's map.  Tokens may lie at
     any one stride (a part of a packed projection), heads packed."""
-    if not isinstance(x, _Tensor) or x.dtype not in _DTYPE:
-        raise TypeError("x must be a torch.bfloat16 or torch.float32 tensor")
-    dev, dt, shape = _given(x, "x", 4), x.dtype, x.shape
-    xp, xs = _rows(x, dt, shape, dev, "x")
-    yp, ys = _rows(y, dt, shape, dev, "y")
-    B, T, H, D = shape
-    fp, rot = _freq(freq, dev)
-    _call_on(dev, stream, "qsa_rope", xp, xs, yp, ys, _DTYPE[dt], B, T, H, D, fp, rot,
-             _layout(layout), mscale, bool(transpose), _arg(pos, _I64T, (B, T), dev, "pos"),
-             _arg(pos0, _I64T, (B,), dev, "pos0"))
+    rc = (_ext or _native()).rope(x, y, freq, pos, pos0, layout, mscale, transpose, stream)
+    if rc:
+        raise QSAError(rc, "qsa_rope")
 
 
 def qsa_qk_norm_rope(q, k, q_out, k_out, freq, v=None, v_out=None, q_weight=None, k_weight=None,
@@ -617,29 +539,10 @@ def qsa_qk_norm_rope(q, k, q_out, k_out, freq, v=None, v_out=None, q_weight=None
     with slot [B,T] int64 the rows slot of caches [B,L,Hkv,D]: per-head RMS norm (where a
     weight [D] fp32 is given), then the rotation; v is copied.  Inputs may be parts of one
     packed projection.  ws: takes the status word (a slot >= L)."""
-    dev = _given(q, "q", 4)
-    qp, qs = _rows(q, _BF, q.shape, dev, "q")
-    B, T, Hq, D = q.shape
-    _given(k, "k", 4)
-    Hkv = k.shape[2]
-    rows = (B, T, Hkv, D)
-    kp, ks = _rows(k, _BF, rows, dev, "k")
-    vp, vs = (None, 0) if v is None else _rows(v, _BF, rows, dev, "v")
-    if (v is None) != (v_out is None):
-        raise ValueError("v and v_out go together")
-    _given(k_out, "k_out", 4)
-    L = T if slot is None else k_out.shape[1]
-    out = (B, L, Hkv, D)
-    wp = None if ws is None else _space(ws, dev)
-    if ws is not None and ws.numel() < 256:
-        raise ValueError("ws must hold the 256-byte status header")
-    fp, rot = _freq(freq, dev)
-    _call_on(dev, stream, "qsa_qk_norm_rope", qp, qs, kp, ks, vp, vs, B, T, Hq, Hkv, D,
-             _arg(q_weight, _F32, (D,), dev, "q_weight"),
-             _arg(k_weight, _F32, (D,), dev, "k_weight"), eps, fp, rot, _layout(layout), mscale,
-             _arg(pos, _I64T, (B, T), dev, "pos"), _arg(pos0, _I64T, (B,), dev, "pos0"),
-             _arg(q_out, _BF, q.shape, dev, "q_out"), _arg(k_out, _BF, out, dev, "k_out"),
-             _arg(v_out, _BF, out, dev, "v_out"), _arg(slot, _I64T, (B, T), dev, "slot"), L, wp)
+    rc = (_ext or _native()).qk_norm_rope(q, k, q_out, k_out, freq, v, v_out, q_weight, k_weight,
+                                          eps, pos, pos0, layout, mscale, slot, ws, stream)
+    if rc:
+        raise QSAError(rc, "qsa_qk_norm_rope")
 
 
 def qsa_qk_norm_rope_backward_workspace_size(B, T, Hq, Hkv, D) -> int:
@@ -652,44 +555,14 @@ def qsa_qk_norm_rope_backward(d_q, d_k, q, k, dq, dk, freq, ws=None, q_weight=No
     """Gradients d_q [B,T,Hq,D], d_k [B,T,Hkv,D] (bf16 or fp32) of qsa_qk_norm_rope's outputs
     -> dq, dk (bf16 or fp32) of its inputs q, k, and dq_weight, dk_weight [D] fp32 of its
     weights (overwritten), where wanted; ws: for the weight gradients."""
-    for t, n in ((d_q, "d_q"), (dq, "dq")):
-        if not isinstance(t, _Tensor) or t.dtype not in _DTYPE:
-            raise TypeError(f"{n} must be a torch.bfloat16 or torch.float32 tensor")
-    dev = _given(q, "q", 4)
-    qp, qs = _rows(q, _BF, q.shape, dev, "q")
-    B, T, Hq, D = q.shape
-    _given(k, "k", 4)
-    Hkv = k.shape[2]
-    rows = (B, T, Hkv, D)
-    kp, ks = _rows(k, _BF, rows, dev, "k")
-    dt, xt = d_q.dtype, dq.dtype
-    fp, rot = _freq(freq, dev)
-    _call_on(dev, stream, "qsa_qk_norm_rope_backward", _arg(d_q, dt, q.shape, dev, "d_q"),
-             _arg(d_k, dt, rows, dev, "d_k"), _DTYPE[dt], qp, qs, kp, ks, B, T, Hq, Hkv, D,
-             _arg(q_weight, _F32, (D,), dev, "q_weight"),
-             _arg(k_weight, _F32, (D,), dev, "k_weight"), eps, fp, rot, _layout(layout), mscale,
-             _arg(pos, _I64T, (B, T), dev, "pos"), _arg(pos0, _I64T, (B,), dev, "pos0"),
-             _arg(dq, xt, q.shape, dev, "dq"), _arg(dk, xt, rows, dev, "dk"), _DTYPE[xt],
-             _arg(dq_weight, _F32, (D,), dev, "dq_weight"),
-             _arg(dk_weight, _F32, (D,), dev, "dk_weight"),
-             None if ws is None else _space(ws, dev), 0 if ws is None else ws.numel())
+    rc = (_ext or _native()).qk_norm_rope_backward(
+        d_q, d_k, q, k, dq, dk, freq, ws, q_weight, k_weight, dq_weight, dk_weight, eps, pos, pos0,
+        layout, mscale, stream)
+    if rc:
+        raise QSAError(rc, "qsa_qk_norm_rope_backward")
 
 
 # ------------------------------------------------ trees of drafted tokens --
-
-def _tree(q, k_cache, v_cache, seqlens, parent, o, ws, n_draft, lse):
-    """Device, sizes and pointers that both tree calls pass."""
-    dev = _given(q, "q", 4)
-    _given(k_cache, "k_cache", 4)
-    B, N, Hq, D = q.shape
-    L, Hkv = k_cache.shape[1], k_cache.shape[2]
-    cache = (B, L, Hkv, D)
-    return (dev, (B, N, Hq, Hkv, D), L, _arg(q, _BF, q.shape, dev, "q"),
-            _arg(k_cache, _BF, cache, dev, "k_cache"), _arg(v_cache, _BF, cache, dev, "v_cache"),
-            _arg(seqlens, _I32, (B,), dev, "seqlens"), _arg(parent, _I32, (B, N), dev, "parent"),
-            _arg(n_draft, _I32, (B,), dev, "n_draft"), _arg(o, _BF, q.shape, dev, "o"),
-            _arg(lse, _F32, (B, N, Hq), dev, "lse"), _space(ws, dev))
-
 
 def qsa_dense_tree_decode_workspace_size(B, N, Hq, Hkv, D) -> int:
     return _size("qsa_dense_tree_decode_workspace_size", B, N, Hq, Hkv, D)
@@ -700,11 +573,10 @@ def qsa_dense_tree_decode(q, k_cache, v_cache, seqlens, parent, o, ws, n_draft=N
     """Drafted tokens q [B,N,Hq,D], the last n_draft[b] (default N) of the seqlens[b] rows of
     caches [B,L,Hkv,D], over the whole prefix and each over its chain of parents [B,N]
     (-1: the last committed token) -> o [B,N,Hq,D]."""
-    dev, sizes, L, qp, kp, vp, sp, pp, np_, op, lp, wp = _tree(q, k_cache, v_cache, seqlens,
-                                                               parent, o, ws, n_draft, lse)
-    scale = sizes[-1] ** -0.5 if scale is None else scale
-    _call_on(dev, stream, "qsa_dense_tree_decode", qp, kp, vp, sp, L, pp, np_, *sizes, scale, op,
-             lp, wp, ws.numel())
+    rc = (_ext or _native()).dense_tree_decode(q, k_cache, v_cache, seqlens, parent, o, ws,
+                                               n_draft, scale, lse, stream)
+    if rc:
+        raise QSAError(rc, "qsa_dense_tree_decode")
 
 
 def qsa_sparse_tree_decode_workspace_size(B, N, Hq, D, r=4, budget=2048) -> int:
@@ -716,20 +588,10 @@ def qsa_sparse_tree_decode(q, k_cache, v_cache, seqlens, sel, parent, o, ws, n_d
     """qsa_dense_tree_decode with each row's prefix cut to its selected blocks sel
     [B,N,budget//r] int32 (any strides but the last; .expand shares one selection) and the
     tokens after the last complete block."""
-    dev, sizes, L, qp, kp, vp, sp, pp, np_, op, lp, wp = _tree(q, k_cache, v_cache, seqlens,
-                                                               parent, o, ws, n_draft, lse)
-    if not isinstance(sel, _Tensor) or sel.dtype is not _I32:
-        raise TypeError("sel must be a torch.int32 tensor")
-    want = (sizes[0], sizes[1], budget // r)
-    if sel.shape != want or sel.get_device() != dev:
-        raise ValueError(f"sel must be {list(want)} on cuda:{dev}, got {list(sel.shape)} on "
-                         f"{sel.device}")
-    sb, sn, se = sel.stride()
-    if want[2] > 1 and se != 1:
-        raise ValueError("sel's entries must be contiguous")
-    scale = sizes[-1] ** -0.5 if scale is None else scale
-    _call_on(dev, stream, "qsa_sparse_tree_decode", qp, kp, vp, sp, L, sel.data_ptr(), sb, sn, pp,
-             np_, *sizes, r, budget, scale, op, lp, wp, ws.numel())
+    rc = (_ext or _native()).sparse_tree_decode(q, k_cache, v_cache, seqlens, parent, o, ws,
+                                                n_draft, scale, lse, sel, r, budget, stream)
+    if rc:
+        raise QSAError(rc, "qsa_sparse_tree_decode")
 
 
 def qsa_check_device_status(ws, stream=None) -> int:

@@ -2,7 +2,9 @@
 
 Each ``csrc/*.cu`` file is compiled to an object under ``_build/`` (in
 parallel, skipped when up to date) and linked, with the CUDA runtime linked
-statically, into ``block_sparse_long_10_b200/libqsa.so``.
+statically, into ``block_sparse_long_10_b200/libqsa.so``.  ``csrc/bind.cpp``, the
+native part of the Python binding, becomes ``_bind.so`` beside it (g++, against
+torch's headers).
 """
 from __future__ import annotations
 
@@ -11,12 +13,15 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqsa.so")
+BIND_SRC = os.path.join(CSRC, "bind.cpp")
+BIND = os.path.join(PKG, "_bind.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + [
@@ -62,15 +67,38 @@ def build(verbose: bool = False, extra: list[str] | None = None, force: bool = F
             os.remove(o)
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
         objs = list(ex.map(lambda s: _compile(s, extra, verbose), srcs))
-    if os.path.exists(LIB) and os.path.getmtime(LIB) >= max(os.path.getmtime(o) for o in objs):
-        return LIB
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
+    if not (os.path.exists(LIB)
+            and os.path.getmtime(LIB) >= max(os.path.getmtime(o) for o in objs)):
+        _link([_nvcc(), *ARCH, "-shared", "-cudart", "static", *objs], LIB, verbose)
+    newest = max(os.path.getmtime(f) for f in (BIND_SRC, os.path.join(ROOT, "include", "qsa.h")))
+    if not (os.path.exists(BIND) and os.path.getmtime(BIND) >= newest):
+        _link(_bind_cmd(), BIND, verbose)
+    return LIB
+
+
+def _link(cmd: list[str], out: str, verbose: bool) -> None:
+    tmp = out + f".tmp{os.getpid()}"
+    cmd = [*cmd, "-o", tmp]
+    if verbose:
+        print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    return LIB
+        raise RuntimeError(f"link of {out} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
+
+
+def _bind_cmd() -> list[str]:
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    inc = [os.path.join(home, "include"), os.path.join(home, "include/torch/csrc/api/include"),
+           os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include"),
+           sysconfig.get_paths()["include"]]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *(f"-I{i}" for i in inc), BIND_SRC, f"-L{PKG}", "-l:libqsa.so", "-Wl,-rpath,$ORIGIN",
+            f"-L{os.path.join(home, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
+            "-lc10"]
 
 
 if __name__ == "__main__":
