@@ -53,6 +53,7 @@ struct Args {
     Lens lens;
     const int32_t *parent;  // [B, N]
     int B, N, Hq, Hkv, G, lg;  // lg: log2 G
+    int k_at, v_at;            // dense: the caches' coordinates in the tensor map
     float scale_log2;
     // prefix parts: part x holds O[x * D ..] and (max, sum)[x * 2 ..]
     float *part, *ml;
@@ -316,8 +317,7 @@ QSA_DEVICE void soft_tile(uint32_t s_tm, uint32_t o_tm, float sc, int left, bool
 
 template <int D, int NT>
 __global__ void __launch_bounds__(THREADS, 1)
-    tree_dense_kernel(const __grid_constant__ CUtensorMap tm_k,
-                      const __grid_constant__ CUtensorMap tm_v, const Args a) {
+    tree_dense_kernel(const __grid_constant__ CUtensorMap tm, const Args a) {
     using C = Cfg<D, NT>;
     constexpr int SL = C::SLOTS;
     extern __shared__ uint8_t smem_raw[];
@@ -360,11 +360,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == SOFT / 32) {
         // ------------------------------------------------------ producer --
         if (lane == 0) {
-            sm100::prefetch_tensormap(&tm_k);
-            sm100::prefetch_tensormap(&tm_v);
+            sm100::prefetch_tensormap(&tm);
             uint32_t it = 0;
             bool dead = false;
-            auto put = [&](const CUtensorMap *m, int64_t tile) {
+            auto put = [&](int cache, int64_t tile) {
                 const uint32_t slot = it % SL;
                 if (dead || !wait(&empty[slot], (it / SL) + 1)) {
                     dead = true;
@@ -373,16 +372,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                 sm100::mbar_arrive_expect_tx(&full[slot], C::TILE);
 #pragma unroll
                 for (int at = 0; at < D / 64; ++at)
-                    sm100::tma_load_3d(ring + slot * C::TILE + at * ATOM, m, sg.g * D + at * 64,
-                                       (int32_t)(tile * KT), (int32_t)sg.b, &full[slot]);
+                    sm100::tma_load_4d(ring + slot * C::TILE + at * ATOM, &tm, sg.g * D + at * 64,
+                                       (int32_t)(tile * KT), (int32_t)sg.b, cache, &full[slot]);
                 ++it;
             };
             while (walk.next(a, sg)) {
-                put(&tm_k, sg.t0);
+                put(a.k_at, sg.t0);
                 for (int j = 0; j < sg.n; ++j) {
-                    if (NT == 1 && j + 1 < sg.n) put(&tm_k, sg.t0 + j + 1);
-                    put(&tm_v, sg.t0 + j);
-                    if (NT == 2 && j + 1 < sg.n) put(&tm_k, sg.t0 + j + 1);
+                    if (NT == 1 && j + 1 < sg.n) put(a.k_at, sg.t0 + j + 1);
+                    put(a.v_at, sg.t0 + j);
+                    if (NT == 2 && j + 1 < sg.n) put(a.k_at, sg.t0 + j + 1);
                 }
             }
             // no copy may land after the CTA has gone
@@ -810,12 +809,11 @@ Workspace sparse_ws(int B, int N, int Hq, int D) {
 }
 
 template <int D, int NT>
-cudaError_t run_dense(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, int ctas,
-                      cudaStream_t s) {
+cudaError_t run_dense(const CUtensorMap &tm, const Args &a, int ctas, cudaStream_t s) {
     auto kern = tree_dense_kernel<D, NT>;
     const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), Cfg<D, NT>::BYTES);
     if (e != cudaSuccess) return e;
-    kern<<<ctas, THREADS, Cfg<D, NT>::BYTES, s>>>(tk, tv, a);
+    kern<<<ctas, THREADS, Cfg<D, NT>::BYTES, s>>>(tm, a);
     return cudaGetLastError();
 }
 
@@ -871,17 +869,16 @@ cudaError_t launch_tree_decode(const uint16_t *q, const uint16_t *k, const uint1
     } else {
         a.units = tree::unit_count(N, a.G);
         a.rows = tree::unit_rows(N, a.G);
-        CUtensorMap tk, tv;
-        if (!tensor_map_cache_bf16(&tk, k, B, L_max, Hkv * D, tree::KT) ||
-            !tensor_map_cache_bf16(&tv, v, B, L_max, Hkv * D, tree::KT))
+        CUtensorMap tm;
+        if (!tensor_map_caches_bf16(&tm, k, v, B, L_max, Hkv * D, tree::KT, &a.k_at, &a.v_at))
             return cudaErrorInvalidValue;
         const bool two = tree::unit_tiles(N, a.G) == 2;
         if (D == 64)
-            e = two ? tree::run_dense<64, 2>(tk, tv, a, sms, s)
-                    : tree::run_dense<64, 1>(tk, tv, a, sms, s);
+            e = two ? tree::run_dense<64, 2>(tm, a, sms, s)
+                    : tree::run_dense<64, 1>(tm, a, sms, s);
         else
-            e = two ? tree::run_dense<128, 2>(tk, tv, a, sms, s)
-                    : tree::run_dense<128, 1>(tk, tv, a, sms, s);
+            e = two ? tree::run_dense<128, 2>(tm, a, sms, s)
+                    : tree::run_dense<128, 1>(tm, a, sms, s);
     }
     if (e != cudaSuccess) return e;
     if (sel) return D == 64 ? tree::run_merge<64, true>(a, s) : tree::run_merge<128, true>(a, s);
