@@ -85,13 +85,14 @@ struct Args {
     TreePrefix tree;         // TREE mode
 };
 
-// A CTA's run of stages over all live rows, nst stages each.
+// A CTA's run of stages over all live rows, nst stages each.  (32 bits: the rows number at
+// most 2^31 / 32, refused beyond; their stages would be 2^31 only with 100 GB of queries.)
 struct TreeRun {
-    int64_t pos, hi, b, b0;  // b0: flat index of sequence b's first stage
-    int64_t P;               // of the current row: committed tokens
-    int i, s0, n, nst;       // draft, first stage, stages
+    int pos, hi, b, b0;  // b0: flat index of sequence b's first stage
+    int64_t P;           // of the current row: committed tokens
+    int i, s0, n, nst;   // draft, first stage, stages
 
-    QSA_DEVICE static int drafts(const TreePrefix &t, int64_t b, int64_t Tk, int64_t &P) {
+    QSA_DEVICE static int drafts(const TreePrefix &t, int b, int64_t Tk, int64_t &P) {
         const int64_t S = t.seqlens[b];
         const int n = t.n_draft ? t.n_draft[b] : t.N;
         P = S - n;
@@ -101,22 +102,26 @@ struct TreeRun {
     // Whole warps; false: nothing for this CTA.
     QSA_DEVICE bool start(const TreePrefix &t, int B, int64_t Tk, int nst_, int lane) {
         nst = nst_;
-        int64_t total = 0, skip;
-        for (int64_t j = lane; j < B; j += 32) total += drafts(t, j, Tk, skip);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        total *= nst;
-        const int64_t ctas = total < gridDim.x ? total : gridDim.x;
-        if (blockIdx.x >= ctas) return false;
-        pos = total * blockIdx.x / ctas;
-        hi = total * (blockIdx.x + 1) / ctas;
+        int total = 0, w0 = 0;
+        int64_t skip;
+        for (int j = 0; j < B; j += 32) {
+            const int w = j + lane < B ? drafts(t, j + lane, Tk, skip) * nst : 0;
+            if (j == 0) w0 = w;
+            total += w;
+        }
+        total = __reduce_add_sync(0xffffffffu, total);
+        const int ctas = total < (int)gridDim.x ? total : gridDim.x, c = blockIdx.x;
+        if (c >= ctas) return false;
+        const int each = total / ctas, more = total - each * ctas;
+        pos = each * c + min(c, more);
+        hi = pos + each + (c < more);
         b0 = 0;
-        for (int64_t j = 0;; j += 32) {
-            const int64_t w = j + lane < B ? (int64_t)drafts(t, j + lane, Tk, skip) * nst : 0;
-            int64_t end = w;
+        for (int j = 0;; j += 32) {
+            const int w = j == 0 ? w0 : j + lane < B ? drafts(t, j + lane, Tk, skip) * nst : 0;
+            int end = w;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, end, o);
+                const int y = __shfl_up_sync(0xffffffffu, end, o);
                 if (lane >= o) end += y;
             }
             const uint32_t past = __ballot_sync(0xffffffffu, b0 + end > pos);
@@ -131,15 +136,15 @@ struct TreeRun {
     }
     QSA_DEVICE bool next(const TreePrefix &t, int64_t Tk) {
         if (pos >= hi) return false;
-        int64_t w = (int64_t)drafts(t, b, Tk, P) * nst;
+        int w = drafts(t, b, Tk, P) * nst;
         while (pos >= b0 + w) {
             b0 += w;
-            w = (int64_t)drafts(t, ++b, Tk, P) * nst;
+            w = drafts(t, ++b, Tk, P) * nst;
         }
-        const int at = (int)(pos - b0);  // N * nst at most
+        const int at = pos - b0;
         i = at / nst;
         s0 = at - i * nst;
-        n = (int)(hi - pos < nst - s0 ? hi - pos : nst - s0);
+        n = min(hi - pos, nst - s0);
         pos += n;
         return true;
     }

@@ -123,42 +123,43 @@ struct Seg {
 // its pipeline, stores a part and loads queries, the time of about START tiles (without
 // them such CTAs were the last by 8 us of 77, at 8 drafts over 32 prefixes of 8K to 16K).
 constexpr int START = 5;
+// (32 bits: a tile is 16 KB of caches and more, times at most 16 units.)
 template <int NT>
 struct Walk {
-    int64_t pos, hi, b, b0;  // b0: flat index of sequence b's first tile
+    int pos, hi, b, b0;  // b0: flat index of sequence b's first tile
 
-    QSA_DEVICE static int64_t tiles(const Seq &s) {
-        return s.P > 0 ? (s.P + KT - 1) / KT + START : 0;
+    QSA_DEVICE static int tiles(const Seq &s) {
+        return s.P > 0 ? (int)((s.P + KT - 1) / KT) + START : 0;
     }
     QSA_DEVICE static int units(const Args &a, const Seq &s) {
         return ((s.n << a.lg) + 128 * NT - 1) / (128 * NT);
     }
-    QSA_DEVICE static int64_t weight(const Args &a, int64_t b) {
+    QSA_DEVICE static int weight(const Args &a, int b) {
         const Seq s = a.lens.at(b);
         return tiles(s) * units(a, s) * a.Hkv;
     }
     // Whole warps; false: nothing for this CTA.
     QSA_DEVICE bool start(const Args &a, int lane) {
-        int64_t total = 0, w0 = 0;
-        for (int64_t i = 0; i < a.B; i += 32) {
-            const int64_t w = i + lane < a.B ? weight(a, i + lane) : 0;
+        int total = 0, w0 = 0;
+        for (int i = 0; i < a.B; i += 32) {
+            const int w = i + lane < a.B ? weight(a, i + lane) : 0;
             if (i == 0) w0 = w;
             total += w;
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        total = __reduce_add_sync(0xffffffffu, total);
         // no CTA without tiles between two of one unit: the merge reads every slot
-        const int64_t ctas = total < gridDim.x ? total : gridDim.x;
-        if (blockIdx.x >= ctas) return false;
-        pos = total * blockIdx.x / ctas;
-        hi = total * (blockIdx.x + 1) / ctas;
+        const int ctas = total < (int)gridDim.x ? total : gridDim.x, c = blockIdx.x;
+        if (c >= ctas) return false;
+        const int each = total / ctas, more = total - each * ctas;
+        pos = each * c + min(c, more);
+        hi = pos + each + (c < more);
         b0 = 0;
-        for (int64_t i = 0;; i += 32) {
-            const int64_t w = i == 0 ? w0 : i + lane < a.B ? weight(a, i + lane) : 0;
-            int64_t end = w;
+        for (int i = 0;; i += 32) {
+            const int w = i == 0 ? w0 : i + lane < a.B ? weight(a, i + lane) : 0;
+            int end = w;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, end, o);
+                const int y = __shfl_up_sync(0xffffffffu, end, o);
                 if (lane >= o) end += y;
             }
             const uint32_t past = __ballot_sync(0xffffffffu, b0 + end > pos);
@@ -174,25 +175,24 @@ struct Walk {
     QSA_DEVICE bool next(const Args &a, Seg &s) {
         while (pos < hi) {
             Seq sq = a.lens.at(b);
-            int64_t nt = tiles(sq), w = nt * units(a, sq) * a.Hkv;
+            int nt = tiles(sq), w = nt * units(a, sq) * a.Hkv;
             while (pos >= b0 + w) {
                 b0 += w;
                 sq = a.lens.at(++b);
                 nt = tiles(sq);
                 w = nt * units(a, sq) * a.Hkv;
             }
-            const int64_t u = (pos - b0) / nt;
-            const int qn = units(a, sq);
-            const int64_t t = pos - b0 - u * nt, n = nt - t < hi - pos ? nt - t : hi - pos;
+            const int u = (pos - b0) / nt, qn = units(a, sq);
+            const int t = pos - b0 - u * nt, n = min(nt - t, hi - pos);
             pos += n;
             if (t + n <= START) continue;  // only tiles that stand for the start
             s.b = b;
             s.P = sq.P;
             s.nd = sq.n;
-            s.g = (int)(u / qn);
-            s.qt = (int)(u - (int64_t)s.g * qn);
+            s.g = u / qn;
+            s.qt = u - s.g * qn;
             s.t0 = t > START ? t - START : 0;
-            s.n = (int)(t + n - START - s.t0);
+            s.n = t + n - START - (int)s.t0;
             s.begins = s.t0 == 0;
             s.ends = t + n == nt;
             return true;
@@ -235,16 +235,52 @@ QSA_DEVICE uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
-// Volatile: left to itself the compiler puts a tile's sums off, and keeps 128 addends.
 QSA_DEVICE uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t d;
-    asm volatile("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
     return d;
+}
+// The largest of three, NaN if one is.
+QSA_DEVICE float max3(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// 2^x for two x <= 2^7 on the FMA pipe: x = j + f with j whole and |f| <= 1/2 (adding 1.5 * 2^23
+// rounds to j and leaves it in the low bits), 2^f by a polynomial of degree 5 fitted to the
+// least largest relative error with 2^0 = 1 exactly (2^-22.6 after fp32's rounding; the
+// exponential unit's is 2^-22), j added to the exponent.  0 from x = -127 on.
+QSA_DEVICE void exp2_fma(uint64_t x2, float &p0, float &p1) {
+    constexpr float SHIFT = 12582912.f;
+    float x0, x1;
+    unpair(x2, x0, x1);
+    const uint64_t x = pair(fmaxf(x0, -127.f), fmaxf(x1, -127.f));
+    const uint64_t t = add2(x, pair(SHIFT, SHIFT));
+    const uint64_t f = fma2(add2(t, pair(-SHIFT, -SHIFT)), pair(-1.f, -1.f), x);
+    uint64_t p = fma2(f, pair(0.001326472614891827f, 0.001326472614891827f),
+                      pair(0.009671512991189957f, 0.009671512991189957f));
+    p = fma2(p, f, pair(0.05550733581185341f, 0.05550733581185341f));
+    p = fma2(p, f, pair(0.24022242426872253f, 0.24022242426872253f));
+    p = fma2(p, f, pair(0.6931470036506653f, 0.6931470036506653f));
+    p = fma2(p, f, pair(1.f, 1.f));
+    float t0, t1;
+    unpair(t, t0, t1);
+    unpair(p, p0, p1);
+    p0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
+    p1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
 }
 
 // Softmax of one row's 128 scores, of which the first `left` count (MASKED): scores in
 // TMEM at s_tm become bf16 probabilities in its first 64 columns; the row's maximum,
 // sum and (at o_tm, if there is one) O move along.  Whole warps.
+//
+// The exponential unit does 16 a clock and SM, so 128 x 128 of them take as long as the
+// tile's two matrix products; POLY of every 8 pairs go to the FMA pipe instead.
+// NaN (and an infinite maximum) must reach the row's output, and exp2_fma does not carry
+// them: they turn the maximum, or what is subtracted, into NaN, and with it every other
+// probability of the row.
+constexpr int POLY = 3;
 template <int D, bool MASKED>
 QSA_DEVICE void soft_tile(uint32_t s_tm, uint32_t o_tm, float sc, int left, bool has_o, float &m,
                           float &l) {
@@ -264,11 +300,11 @@ QSA_DEVICE void soft_tile(uint32_t s_tm, uint32_t o_tm, float sc, int left, bool
         }
 #pragma unroll
         for (int e = 0; e < 32; e += 2)
-            mx[(e >> 1) & 3] = fmaxf(mx[(e >> 1) & 3],
-                                     fmaxf(__uint_as_float(y[e]), __uint_as_float(y[e + 1])));
+            mx[(e >> 1) & 3] =
+                max3(mx[(e >> 1) & 3], __uint_as_float(y[e]), __uint_as_float(y[e + 1]));
     }
-    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-    const bool grow = mt > m + GROWTH;
+    const float mt = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * sc;
+    const bool grow = !(mt <= m + GROWTH);  // or NaN
     if (__any_sync(0xffffffffu, grow)) {
         const float mn = grow ? mt : m;
         const float f = grow ? fast_exp2(m - mn) : 1.f;
@@ -285,7 +321,7 @@ QSA_DEVICE void soft_tile(uint32_t s_tm, uint32_t o_tm, float sc, int left, bool
             }
         }
     }
-    const float mu = m == -INFINITY ? 0.f : m;
+    const float mu = m == -INFINITY ? 0.f : m + (m - m);
     const uint64_t sc2 = pair(sc, sc), mu2 = pair(-mu, -mu);
     uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -297,9 +333,15 @@ QSA_DEVICE void soft_tile(uint32_t s_tm, uint32_t o_tm, float sc, int left, bool
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
             float p0, p1;
-            unpair(fma2(pair(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), sc2, mu2), p0, p1);
-            p0 = fast_exp2(p0);
-            p1 = fast_exp2(p1);
+            const uint64_t z =
+                fma2(pair(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), sc2, mu2);
+            if ((e >> 1) % 8 * POLY % 8 < POLY) {
+                exp2_fma(z, p0, p1);
+            } else {
+                unpair(z, p0, p1);
+                p0 = fast_exp2(p0);
+                p1 = fast_exp2(p1);
+            }
             if (MASKED) {  // 0 * -inf at a scale of 0
                 if (c + e >= left) p0 = 0.f;
                 if (c + e + 1 >= left) p1 = 0.f;
