@@ -152,7 +152,8 @@ struct TreePrefix {
     const int32_t *sel;                // row (b, i) at b * sel_b + i * sel_n
     int64_t sel_b, sel_n;
     float *o, *ml;                     // part (CTA + row) * Hq + h
-    int32_t *first, *last;             // [rows]: first and last CTA of a row
+    int32_t *first, *last;             // first and last CTA of a row, `stride` between rows
+    int stride;
 };
 int tree_sparse_ctas(int num_sms);
 cudaError_t launch_tree_sparse_prefix(const uint16_t *q, const uint16_t *k, const uint16_t *v,

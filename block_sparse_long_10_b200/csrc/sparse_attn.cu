@@ -187,8 +187,8 @@ __global__ void __launch_bounds__(THREADS, Ring<MODE>::CTAS) sparse_attn_kernel(
             e1 = min(e0 + run.n * C::NBS, a.kb);
             qrow = a.q + row * Hq * D;
             if (tid == 0) {
-                if (run.s0 == 0) a.tree.first[row] = blockIdx.x;
-                if (e1 == a.kb) a.tree.last[row] = blockIdx.x;
+                if (run.s0 == 0) a.tree.first[row * a.tree.stride] = blockIdx.x;
+                if (e1 == a.kb) a.tree.last[row * a.tree.stride] = blockIdx.x;
             }
         } else {
             b = item / a.nsplit;

@@ -7,13 +7,14 @@
 // blocks and the unpooled tail (sparse), and to its own chain i, parent[i],
 // parent[parent[i]], ...: softmax over both parts together.
 //
-// The two parts are kept apart.  The dense prefix has no mask that differs between
-// rows: it is two matrix products (tree_dense_kernel).  Selections differ from row to
-// row: they are gathered row by row (sparse_attn.cu).  The chain is a handful of
-// tokens with a mask of its own per row: it is walked token by token in fp32, so what a
-// masked draft's cache rows hold (infinities, NaN) never enters another branch, as a
-// zero times it in a matrix product would.  Both parts leave (max, sum, O) in base 2
-// and meet in tree_merge_kernel.
+// What the cache rows of other branches hold (infinities, NaN) never enters a row, as a
+// zero times it in a matrix product would, and does not change its bits.  Dense, the drafts
+// lie behind the prefix in the same tiles: two matrix products (tree_dense_kernel) with a
+// mask of ancestors, in which values of drafts that are not finite count as zeros; the
+// merge adds them to the rows whose chains they are in.  Selections differ from row to row:
+// they are gathered row by row (sparse_attn.cu), and the merge walks the chains, token by
+// token, in fp32.  All parts of a row are (max, sum, O) in base 2 and meet in
+// tree_merge_kernel.
 #include "qsa_common.cuh"
 #include "qsa_launch.h"
 #include "sm100.cuh"
@@ -46,6 +47,15 @@ struct Lens {
     }
 };
 
+constexpr int KT = 128;  // tokens per tile (dense)
+constexpr int DRAFT_TILES = (MAX_N + KT - 2) / KT + 1;  // that drafts can lie in
+
+// What the prefix kernel leaves of a unit for the merge.
+struct UnitInfo {
+    int32_t first, last;             // CTAs that have tiles of it
+    int32_t cleared[DRAFT_TILES];    // dense: that tile has drafts' values that are not finite
+};
+
 struct Args {
     const uint16_t *q;   // [B, N, Hq, D]
     const uint16_t *k;   // [B, L_max, Hkv, D]
@@ -60,7 +70,7 @@ struct Args {
     // Units: dense, `rows` (draft, head) pairs of a KV head, `units` to a (sequence, KV head);
     // sparse, the heads of a draft.  CTA c leaves unit u's row r in part (c + u) * rows + r.
     int units, rows;
-    int32_t *first, *last;  // first and last CTA of each unit
+    UnitInfo *info;
     uint16_t *o;
     float *lse;
     void *status;
@@ -68,7 +78,7 @@ struct Args {
 
 // ------------------------------------------------------------ dense prefix --
 // Rows of one KV head, (draft, head) pairs r = i * G + h, are cut into units of
-// 128 * NT.  A unit times a run of 128-token tiles of its prefix is a flash attention
+// 128 * NT.  A unit times a run of 128-token tiles of its sequence is a flash attention
 // on the tensor cores: S = Q K^T and O += P V with 128 x 128 x 16 MMAs (tcgen05), S, P
 // and O in TMEM, a thread per row for the softmax.
 //
@@ -86,10 +96,9 @@ struct Args {
 // factor 256) since its last rescale: sums and O stay far inside fp32, and P keeps bf16's
 // relative precision at any size.  P is rounded to bf16 for the matrix product; the sum
 // is taken of the unrounded values, in fp32.
-constexpr int KT = 128;        // tokens per tile
 constexpr int ATOM = KT * 128; // bytes of a 64-column half tile in shared memory
 constexpr int SOFT = 256;      // softmax threads
-constexpr int THREADS = SOFT + 64;
+constexpr int THREADS = SOFT + 96;   // and a producer, an MMA and a cleaning warp
 constexpr float GROWTH = 8.f;
 constexpr int MAX_CTAS = 160;  // what the workspace is sized for
 constexpr uint64_t WAIT_NS = 2000000000ull;
@@ -103,7 +112,7 @@ struct Cfg {
     static constexpr int SLOTS = FIT > 8 ? 8 : FIT;
     static constexpr int OFF_BAR = OFF_RING + SLOTS * TILE;
     static constexpr int BYTES = 1024 + OFF_BAR + 512;
-    static_assert((2 * SLOTS + 6) * 8 + 16 <= 512, "barriers");
+    static_assert((3 * SLOTS + 6) * 8 + 16 <= 512, "barriers");
     static_assert(NT == 2 || 2 * 128 * 8 <= TILE, "the streams' sums fit in the query tile");
     // TMEM columns
     static constexpr int O_COL = 256;
@@ -129,7 +138,7 @@ struct Walk {
     int pos, hi, b, b0;  // b0: flat index of sequence b's first tile
 
     QSA_DEVICE static int tiles(const Seq &s) {
-        return s.P > 0 ? (int)((s.P + KT - 1) / KT) + START : 0;
+        return s.n > 0 ? (int)((s.P + s.n + KT - 1) / KT) + START : 0;
     }
     QSA_DEVICE static int units(const Args &a, const Seq &s) {
         return ((s.n << a.lg) + 128 * NT - 1) / (128 * NT);
@@ -271,9 +280,23 @@ QSA_DEVICE void exp2_fma(uint64_t x2, float &p0, float &p1) {
     p1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
 }
 
-// Softmax of one row's 128 scores, of which the first `left` count (MASKED): scores in
-// TMEM at s_tm become bf16 probabilities in its first 64 columns; the row's maximum,
-// sum and (at o_tm, if there is one) O move along.  Whole warps.
+// Scores without a bit in `ok` become -inf.  Whole warps.
+QSA_DEVICE void mask_tile(uint32_t s_tm, const uint32_t (&ok)[4]) {
+#pragma unroll
+    for (int c = 0; c < KT; c += 32) {
+        uint32_t y[32];
+        sm100::tmem_ld32(s_tm + c, y);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (!(ok[c / 32] >> e & 1)) y[e] = 0xff800000u;
+        sm100::tmem_st32(s_tm + c, y);
+    }
+    sm100::tmem_wait_st();
+}
+
+// Softmax of one row's 128 scores: scores in TMEM at s_tm become bf16 probabilities in its
+// first 64 columns; the row's maximum, sum and (at o_tm, if there is one) O move along.
+// Whole warps.
 //
 // The exponential unit does 16 a clock and SM, so 128 x 128 of them take as long as the
 // tile's two matrix products; POLY of every 8 pairs go to the FMA pipe instead.
@@ -281,9 +304,8 @@ QSA_DEVICE void exp2_fma(uint64_t x2, float &p0, float &p1) {
 // them: they turn the maximum, or what is subtracted, into NaN, and with it every other
 // probability of the row.
 constexpr int POLY = 3;
-template <int D, bool MASKED>
-QSA_DEVICE void soft_tile(uint32_t s_tm, uint32_t o_tm, float sc, int left, bool has_o, float &m,
-                          float &l) {
+template <int D>
+QSA_DEVICE void soft_tile(uint32_t s_tm, uint32_t o_tm, float sc, bool has_o, float &m, float &l) {
     // The scores are read twice, 32 at a time: all 128 in registers would spill.
     uint32_t x[2][32];
     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -293,11 +315,6 @@ QSA_DEVICE void soft_tile(uint32_t s_tm, uint32_t o_tm, float sc, int left, bool
         uint32_t(&y)[32] = x[(c >> 5) & 1];
         sm100::tmem_ld32_end(y);
         sm100::tmem_ld32_begin(s_tm + (c + 32) % KT, x[1 - ((c >> 5) & 1)]);
-        if (MASKED) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-                if (c + e >= left) y[e] = 0xff800000u;  // -inf
-        }
 #pragma unroll
         for (int e = 0; e < 32; e += 2)
             mx[(e >> 1) & 3] =
@@ -342,10 +359,6 @@ QSA_DEVICE void soft_tile(uint32_t s_tm, uint32_t o_tm, float sc, int left, bool
                 p0 = fast_exp2(p0);
                 p1 = fast_exp2(p1);
             }
-            if (MASKED) {  // 0 * -inf at a scale of 0
-                if (c + e >= left) p0 = 0.f;
-                if (c + e + 1 >= left) p1 = 0.f;
-            }
             sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair(p0, p1));
             pk[e / 2] = pack_bf16x2(p0, p1);
         }
@@ -357,6 +370,62 @@ QSA_DEVICE void soft_tile(uint32_t s_tm, uint32_t o_tm, float sc, int left, bool
     sm100::tmem_wait_st();
 }
 
+// A pair of bf16 with what is not finite cleared; sets `some` if anything was.
+QSA_DEVICE uint32_t finite_pair(uint32_t w, bool &some) {
+    const bool lo = (w & 0x7F80u) == 0x7F80u, hi = (w & 0x7F800000u) == 0x7F800000u;
+    some |= lo || hi;
+    return w & (lo ? 0xFFFF0000u : ~0u) & (hi ? 0x0000FFFFu : ~0u);
+}
+// In a V tile, clears what is not finite in rows d0 .. d1 - 1 and all of the rows behind
+// them.  One warp; true if this lane met something that was not finite.
+template <int D>
+QSA_DEVICE bool clean_rows(uint8_t *vt, int d0, int d1, int lane) {
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    bool some = false;
+#pragma unroll 1
+    for (int at = 0; at < D / 64; ++at) {
+        uint4 *v = reinterpret_cast<uint4 *>(vt + at * ATOM);
+#pragma unroll 4
+        for (int i = d0 * 8 + lane; i < d1 * 8; i += 32) {
+            uint4 x = v[i];
+            bool bad = false;
+            x.x = finite_pair(x.x, bad);
+            x.y = finite_pair(x.y, bad);
+            x.z = finite_pair(x.z, bad);
+            x.w = finite_pair(x.w, bad);
+            if (bad) v[i] = x;
+            some |= bad;
+        }
+#pragma unroll 4
+        for (int i = d1 * 8 + lane; i < KT * 8; i += 32) v[i] = zero;
+    }
+    return some;
+}
+// Tile j of the segment reaches behind the prefix.
+QSA_DEVICE bool has_drafts(const Seg &sg, int j) { return (sg.t0 + j + 1) * KT > sg.P; }
+
+// The tokens of a tile that draft i (-1: none) attends to: the pl (or, below 0, none) that
+// are committed, and of the drafts, 0 being token pl, itself and its ancestors.  A parent
+// must come before its child; any other value ends the chain.
+QSA_DEVICE void visible(const Args &a, const Seg &sg, int i, int pl, uint32_t (&ok)[4]) {
+    const int32_t *parent = a.parent + sg.b * a.N;
+    int j = i;
+#pragma unroll
+    for (int w = 3; w >= 0; --w) {
+        const int lo = 32 * w - pl;  // the draft at the word's first token
+        // (from above the tile, too: a child may lie there)
+        uint32_t m = lo >= 0 ? 0u : lo <= -32 ? ~0u : (1u << -lo) - 1;
+        while (j >= max(lo, 0)) {
+            if (j - lo < 32) m |= 1u << (j - lo);
+            const int p = parent[j];
+            const bool wrong = (uint32_t)(p + 1) > (uint32_t)j;
+            if (wrong && j == i) record_status(a.status, QSA_ERR_DEVICE);
+            j = wrong ? -1 : p;
+        }
+        ok[w] = m;
+    }
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(THREADS, 1)
     tree_dense_kernel(const __grid_constant__ CUtensorMap tm, const Args a) {
@@ -365,7 +434,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR), *empty = full + SL;
-    uint64_t *sfull = empty + SL, *pready = sfull + 2, *odone = pready + 2, *qready = odone + 1;
+    uint64_t *clean = empty + SL;  // values of drafts are
+    uint64_t *sfull = clean + SL, *pready = sfull + 2, *odone = pready + 2, *qready = odone + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(qready + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -378,6 +448,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = 0; i < SL; ++i) {
             sm100::mbar_init(&full[i], 1);
             sm100::mbar_init(&empty[i], 1);
+            sm100::mbar_init(&clean[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             sm100::mbar_init(&sfull[i], 1);
@@ -436,7 +507,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // one lane issues.
         const bool leader = sm100::elect_one();
         const uint32_t qs = smem_u32(sm);
-        uint32_t base = 0, done[2] = {0, 0}, segs = 0;
+        uint32_t base = 0, done[2] = {0, 0}, segs = 0, cleaned = 0;
         while (walk.next(a, sg)) {
             const int n = __shfl_sync(0xffffffffu, sg.n, 0), steps = NT * n;
             wait(qready, segs);
@@ -463,7 +534,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int s = t & 1;
                 const uint32_t idx = ring_v<NT>(base, NT == 2 ? t >> 1 : t, n), slot = idx % SL;
                 wait(&pready[s], done[s]++);
-                if (NT == 1 || s == 0) wait(&full[slot], idx / SL);
+                if (NT == 1 || s == 0) {
+                    if (has_drafts(sg, NT == 2 ? t >> 1 : t)) {
+                        wait(&clean[slot], cleaned >> slot);
+                        cleaned ^= 1u << slot;
+                    }
+                    wait(&full[slot], idx / SL);
+                }
                 sm100::tc_fence_after();
                 const uint64_t va = sm100::smem_desc_mnmajor(ring + slot * C::TILE, ATOM);
                 if (leader) {
@@ -479,12 +556,38 @@ __global__ void __launch_bounds__(THREADS, 1)
             base += 2 * n;
             ++segs;
         }
+    } else if (warp == SOFT / 32 + 2) {
+        // ---------------------------------------------------------- clean --
+        // V rows of drafts, before they meet zeros: no infinity, no NaN; and none at all
+        // behind the drafts.  (A slot is used again only after its product, so the slots'
+        // barriers are never two phases ahead.)
+        uint32_t base = 0;
+        while (walk.next(a, sg)) {
+            const int64_t u = (sg.b * a.Hkv + sg.g) * a.units + sg.qt;
+            for (int j = 0; j < sg.n; ++j) {
+                if (!has_drafts(sg, j)) continue;
+                const int64_t pl = sg.P - (sg.t0 + j) * KT, sl = pl + sg.nd;
+                const uint32_t idx = ring_v<NT>(base, j, sg.n), slot = idx % SL;
+                wait(&full[slot], idx / SL);
+                uint8_t *vt = sm + C::OFF_RING + slot * C::TILE;
+                const bool some = clean_rows<D>(vt, pl > 0 ? (int)pl : 0, sl < KT ? (int)sl : KT,
+                                                lane);
+                sm100::fence_async_shared();
+                const bool any = __any_sync(0xffffffffu, some);
+                if (lane == 0) {
+                    a.info[u].cleared[sg.t0 + j - sg.P / KT] = any;
+                    sm100::mbar_arrive(&clean[slot]);
+                }
+            }
+            base += 2 * sg.n;
+        }
     } else {
         // ------------------------------------------------------- softmax --
         const int s = warp >> 2, r = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's quarter of TMEM
         const uint32_t s_tm = tmem + lanes + s * KT, o_tm = tmem + lanes + C::O_COL + s * D;
-        const float sc = fabsf(a.scale_log2);
+        // at least FLT_MIN, so that a masked score's -inf stays one at a scale of 0
+        const float sc = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
         const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // the sign moves into Q
         constexpr int QB = D / 16;  // loads in flight
         float2 *s_ml = reinterpret_cast<float2 *>(sm);  // [2][128]: the query tile, once done with
@@ -520,35 +623,23 @@ __global__ void __launch_bounds__(THREADS, 1)
             sm100::mbar_arrive(qready);
             if (tid == 0) {
                 const int64_t u = (sg.b * a.Hkv + sg.g) * a.units + sg.qt;
-                if (sg.begins) a.first[u] = blockIdx.x;
-                if (sg.ends) a.last[u] = blockIdx.x;
+                if (sg.begins) a.info[u].first = blockIdx.x;
+                if (sg.ends) a.info[u].last = blockIdx.x;
             }
             const int row = r0 + (NT == 2 ? s * 128 : 0) + r;
             const bool on = __any_sync(0xffffffffu, row < R);  // a live row in this warp
             float m = -INFINITY, l = 0.f;
             for (int t = s; t < steps; t += 2) {
                 const int j = NT == 2 ? t >> 1 : t;
-                const int64_t left = sg.P - (sg.t0 + j) * KT;  // tokens in this tile
+                uint32_t ok[4];
+                const bool drafts = has_drafts(sg, j);
+                if (drafts)  // the mask while the tile is on its way
+                    visible(a, sg, row < R ? row >> a.lg : -1, (int)(sg.P - (sg.t0 + j) * KT), ok);
                 wait(&sfull[s], got++);
                 sm100::tc_fence_after();
                 if (on) {
-                    if (left < KT)
-                        soft_tile<D, true>(s_tm, o_tm, sc, (int)left, t > 1, m, l);
-                    else
-                        soft_tile<D, false>(s_tm, o_tm, sc, KT, t > 1, m, l);
-                }
-                if (left < KT && (NT == 1 || s == 0)) {
-                    // rows behind the prefix may hold anything: 0 * V must be 0
-                    const uint32_t idx = ring_v<NT>(base, j, sg.n), slot = idx % SL;
-                    wait(&full[slot], idx / SL);
-                    uint8_t *vt = sm + C::OFF_RING + slot * C::TILE;
-                    const int dead = KT - (int)left;  // rows, 8 chunks in each half tile
-                    for (int i = r; i < dead * (D / 8); i += 128) {
-                        const int at = i / (dead * 8), w = i - at * dead * 8;
-                        *reinterpret_cast<uint4 *>(vt + at * ATOM + (int)left * 128 + w * 16) =
-                            make_uint4(0, 0, 0, 0);
-                    }
-                    sm100::fence_async_shared();
+                    if (drafts) mask_tile(s_tm, ok);
+                    soft_tile<D>(s_tm, o_tm, sc, t > 1, m, l);
                 }
                 sm100::tc_fence_before();
                 sm100::mbar_arrive(&pready[s]);
@@ -660,8 +751,8 @@ struct Row {
         for (int e = 0; e < E; ++e) o[e] = o[e] * fa + o2[e] * fb;
         m = mn;
     }
-    // a token's cache rows; `on` false: the group sits out (all lanes call)
-    QSA_DEVICE void token(const Raw &k, const Raw &v, bool on, float scale_log2) {
+    // a key's score (all lanes call)
+    QSA_DEVICE float score(const Raw &k, float scale_log2) const {
         float f[E];
         float x = 0.f;
         k.get(f);
@@ -670,9 +761,24 @@ struct Row {
         x += __shfl_xor_sync(0xffffffffu, x, 1);
         x += __shfl_xor_sync(0xffffffffu, x, 2);
         x += __shfl_xor_sync(0xffffffffu, x, 4);
+        return x * scale_log2;
+    }
+    // a token's cache rows; `on` false: the group sits out (all lanes call)
+    QSA_DEVICE void token(const Raw &k, const Raw &v, bool on, float scale_log2) {
+        const float x = score(k, scale_log2);
         if (!on) return;
+        float f[E];
         v.get(f);
-        join(x * scale_log2, 1.f, f);
+        join(x, 1.f, f);
+    }
+    // of a token that is in m and l already, the values that are not finite
+    QSA_DEVICE void patch(const Raw &k, const Raw &v, float scale_log2) {
+        const float p = fast_exp2(score(k, scale_log2) - (m == -INFINITY ? 0.f : m));
+        float f[E];
+        v.get(f);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (!(fabsf(f[e]) < INFINITY)) o[e] += p * f[e];
     }
     // the warp's four groups' parts become one, in every lane
     QSA_DEVICE void join_groups() {
@@ -688,12 +794,12 @@ struct Row {
     }
 };
 
-// W warps per (row, head): their 4 W groups of 8 lanes share out the chain's tokens and
-// (after the prefix kernel) the prefix parts, the next ones' loads under the current
-// ones' arithmetic.  W = 1 takes the heads of one KV head into a block, whose loads of
-// the chain meet in L1.
+// W warps per (row, head): their 4 W groups of 8 lanes share out the parts and (sparse, before
+// the prefix kernel has ended) the chain's tokens, the next ones' loads under the current
+// ones' arithmetic.  W = 1 takes the heads of one KV head into a
+// block, whose loads of the chain meet in L1.
 template <int D, bool SPARSE, int W>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const Args a) {
+__global__ void __launch_bounds__(256, 3) tree_merge_kernel(const Args a) {
     constexpr int E = Row<D>::E;
     __shared__ float s_o[W > 1 ? W : 1][W > 1 ? D : 1], s_m[W], s_l[W];
     const int64_t row = blockIdx.x;
@@ -713,21 +819,22 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const Args a) {
     r.start(a.q + (row * a.Hq + h) * D, li);
     const int64_t tok = (int64_t)a.Hkv * D;
     const int64_t base = (b * a.lens.L_max + sq.P) * tok + (h >> a.lg) * D + li * E;
-    int j = sq.bad ? -1 : i;
-    // the next 4 W drafts of the chain: this group's, or -1.  A parent must come before
-    // its child; any other value ends the chain.
-    auto walk = [&]() {
-        int mine = -1;
-        for (int s = 0; s < 4 * W && j >= 0; ++s) {
-            if (s == grp) mine = j;
-            const int p = parent[j];
-            const bool wrong = p < -1 || p >= j;
-            if (wrong && j == i && lane == 0) record_status(a.status, QSA_ERR_DEVICE);
-            j = wrong ? -1 : p;
-        }
-        return mine;
+    // A parent must come before its child; any other value ends the chain.
+    auto above = [&](int j) {
+        const int p = parent[j];
+        const bool wrong = p < -1 || p >= j;
+        if (wrong && j == i && lane == 0) record_status(a.status, QSA_ERR_DEVICE);
+        return wrong ? -1 : p;
     };
-    {
+    if (SPARSE && !sq.bad) {
+        int j = i;
+        // the next 4 W drafts of the chain: this group's, or -1
+        auto walk = [&]() {
+            int mine = -1;
+            for (int s = 0; s < 4 * W && j >= 0; ++s, j = above(j))
+                if (s == grp) mine = j;
+            return mine;
+        };
         int mine = walk();
         typename Row<D>::Raw k, v;
         const int64_t at0 = base + (mine < 0 ? 0 : mine) * tok;
@@ -746,16 +853,20 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const Args a) {
             r.token(k1, v1, on, a.scale_log2);
         }
     }
-    griddep_wait();  // the prefix parts
+    griddep_wait();  // the prefix kernel's parts
     int64_t x0 = 0;
     int parts = 0;
-    if (SPARSE ? !sq.bad : sq.P > 0) {
+    bool patch = false;  // values of drafts were not finite
+    if (!sq.bad) {
         // unit and row in it
         const int rr = SPARSE ? h : (i << a.lg) + (h & (a.G - 1)), qt = rr / a.rows;
         const int64_t u = SPARSE ? row : (b * a.Hkv + (h >> a.lg)) * a.units + qt;
-        const int first = a.first[u];
-        x0 = (first + u) * a.rows + (rr - qt * a.rows);
-        parts = a.last[u] - first + 1;
+        const UnitInfo &info = a.info[u];
+        x0 = (info.first + u) * a.rows + (rr - qt * a.rows);
+        parts = info.last - info.first + 1;
+        if (!SPARSE)
+            for (int k = 0; k <= (int)((sq.P + sq.n - 1) / KT - sq.P / KT); ++k)
+                patch |= info.cleared[k] != 0;
     }
     float2 ml;
     float4 f[E / 4];
@@ -808,6 +919,14 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const Args a) {
         }
         r.join_groups();
     }
+    // what was cleared in the chain's values, all groups the same token
+    if (!SPARSE && patch)
+        for (int j = i; j >= 0; j = above(j)) {
+            typename Row<D>::Raw k, v;
+            k.load(a.k + base + j * tok);
+            v.load(a.v + base + j * tok);
+            r.patch(k, v, a.scale_log2);
+        }
     if (lane < 8) {
         const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
         uint16_t *orow = a.o + (row * a.Hq + h) * D + li * E;
@@ -834,11 +953,10 @@ int unit_rows(int N, int G) {
 int unit_count(int N, int G) { return (N * G + unit_rows(N, G) - 1) / unit_rows(N, G); }
 
 struct Workspace {
-    size_t first, last, part, ml, bytes;
+    size_t info, part, ml, bytes;
     Workspace(size_t ctas, size_t units, size_t rows, size_t D) {
-        first = kWsHeader;
-        last = first + (units * 4 + 255) / 256 * 256;
-        part = last + (units * 4 + 255) / 256 * 256;
+        info = kWsHeader;
+        part = info + (units * sizeof(UnitInfo) + 255) / 256 * 256;
         ml = part + (ctas + units) * rows * D * 4;
         bytes = ml + (ctas + units) * rows * 8;
     }
@@ -896,8 +1014,7 @@ cudaError_t launch_tree_decode(const uint16_t *q, const uint16_t *k, const uint1
     a.scale_log2 = scale * tree::LOG2E; a.o = o; a.lse = lse; a.status = ws;
     const tree::Workspace x =
         sel ? tree::sparse_ws(B, N, Hq, D) : tree::dense_ws(B, N, Hkv, a.G, D);
-    a.first = reinterpret_cast<int32_t *>(w + x.first);
-    a.last = reinterpret_cast<int32_t *>(w + x.last);
+    a.info = reinterpret_cast<tree::UnitInfo *>(w + x.info);
     a.part = reinterpret_cast<float *>(w + x.part);
     a.ml = reinterpret_cast<float *>(w + x.ml);
     const int sms = num_sms < tree::MAX_CTAS ? num_sms : tree::MAX_CTAS;
@@ -905,7 +1022,8 @@ cudaError_t launch_tree_decode(const uint16_t *q, const uint16_t *k, const uint1
     if (sel) {
         a.units = 1;
         a.rows = Hq;
-        const TreePrefix t{seqlens, n_draft, N, sel, sel_b, sel_n, a.part, a.ml, a.first, a.last};
+        const TreePrefix t{seqlens, n_draft, N, sel, sel_b, sel_n, a.part, a.ml, &a.info->first, &a.info->last,
+                           sizeof(tree::UnitInfo) / 4};
         e = launch_tree_sparse_prefix(q, k, v, t, L_max, kb, B, Hq, Hkv, D, scale,
                                       tree_sparse_ctas(sms), s);
     } else {
