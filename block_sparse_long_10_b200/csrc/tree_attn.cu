@@ -280,16 +280,19 @@ QSA_DEVICE void exp2_fma(uint64_t x2, float &p0, float &p1) {
     p1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
 }
 
-// Scores without a bit in `ok` become -inf.  Whole warps.
+// Scores without a bit in `ok` become -inf.  Whole warps.  A loop, not unrolled code: it runs
+// once or twice in a kernel, and fetching its instructions was most of its time.
 QSA_DEVICE void mask_tile(uint32_t s_tm, const uint32_t (&ok)[4]) {
-#pragma unroll
-    for (int c = 0; c < KT; c += 32) {
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        const uint32_t bits = c == 0 ? ok[0] : c == 1 ? ok[1] : c == 2 ? ok[2] : ok[3];
+        if (__all_sync(0xffffffffu, bits == ~0u)) continue;
         uint32_t y[32];
-        sm100::tmem_ld32(s_tm + c, y);
+        sm100::tmem_ld32(s_tm + c * 32, y);
 #pragma unroll
         for (int e = 0; e < 32; ++e)
-            if (!(ok[c / 32] >> e & 1)) y[e] = 0xff800000u;
-        sm100::tmem_st32(s_tm + c, y);
+            if (!(bits >> e & 1)) y[e] = 0xff800000u;
+        sm100::tmem_st32(s_tm + c * 32, y);
     }
     sm100::tmem_wait_st();
 }
@@ -597,6 +600,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int R = sg.nd * a.G, r0 = sg.qt * 128 * NT;
             const uint16_t *qb = a.q + (sg.b * a.N * a.Hq + sg.g * a.G) * D;
             if (segs > 0) soft_sync();  // the sums have been read
+            if (sg.ends && tid < sg.nd)  // into L1, for the masks
+                asm volatile("{\n\t.reg .b32 x;\n\tld.global.ca.b32 x, [%0];\n\t}\n" ::"l"(
+                                 a.parent + sg.b * a.N + tid)
+                             : "memory");
             // all of a thread's loads at once: one after the other they took 7 us
 #pragma unroll 1
             for (int i0 = tid; i0 < NT * 128 * (D / 8); i0 += SOFT * QB) {
@@ -977,11 +984,12 @@ cudaError_t run_dense(const CUtensorMap &tm, const Args &a, int ctas, cudaStream
     return cudaGetLastError();
 }
 
-// Few (row, head) pairs (under 8 warps an SM) have many parts each: 8 warps a pair.
+// 8 warps a (row, head) pair where all pairs' blocks run at once (3 on each of 148 SMs): few
+// pairs may have many parts each.
 template <int D, bool SPARSE>
 cudaError_t run_merge(const Args &a, cudaStream_t s) {
     const int64_t rows = (int64_t)a.B * a.N;
-    if (rows * a.Hq < 148 * 8)
+    if (rows * a.Hq <= 148 * 3)
         return launch_dependent(tree_merge_kernel<D, SPARSE, 8>, dim3((unsigned)rows, a.Hq),
                                 dim3(256), 0, s, a);
     return launch_dependent(tree_merge_kernel<D, SPARSE, 1>, dim3((unsigned)rows, a.Hkv),
