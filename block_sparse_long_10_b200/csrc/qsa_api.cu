@@ -618,7 +618,7 @@ static qsa_status_t check_tree(const void *q, const void *k, const void *v, cons
         !isfinite(scale))
         return QSA_ERR_INVALID_ARG;
     if (!q || !k || !v || !seqlens || !parent || !o) return QSA_ERR_INVALID_ARG;
-    if (!supported_attn(Hq, Hkv, D) || N > qsa::tree_max_drafts() ||
+    if (!supported_attn(Hq, Hkv, D) || N > qsa::TREE_DRAFTS ||
         (int64_t)B * N > INT32_MAX / 32 || L_max > INT32_MAX)
         return QSA_ERR_UNSUPPORTED_SHAPE;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o))

@@ -143,23 +143,26 @@ cudaError_t launch_norm_rope_grad(const void *d_q, const void *d_k, bool d_fp32,
                                   float *dqw, float *dkw, void *ws, int num_sms,
                                   cudaStream_t s);
 
-// Attention for a tree of drafted tokens (tree_attn.cu): the prefix parts, here over
-// selected blocks (sparse_attn.cu), and what merges them with the drafts' chains.
-// Part x of a (row, head): O at o[x * D], (max, sum) at ml[x * 2], in base 2.
+// Attention for a tree of drafted tokens (tree_attn.cu), over selected blocks its parts
+// (sparse_attn.cu).  Part x of a (row, head): O at o[x * D], (max, sum) at ml[x * 2], in
+// base 2.
+constexpr int TREE_DRAFTS = 256;       // per sequence
 struct TreePrefix {
     const int32_t *seqlens, *n_draft;  // [B]; n_draft may be nullptr
+    const int32_t *parent;             // [B, N]
     int N;
-    const int32_t *sel;                // row (b, i) at b * sel_b + i * sel_n
+    const int32_t *sel;                // kb entries of row (b, i) at b * sel_b + i * sel_n
     int64_t sel_b, sel_n;
+    int kb;
     float *o, *ml;                     // part (CTA + row) * Hq + h
     int32_t *first, *last;             // first and last CTA of a row, `stride` between rows
     int stride;
 };
 int tree_sparse_ctas(int num_sms);
 cudaError_t launch_tree_sparse_prefix(const uint16_t *q, const uint16_t *k, const uint16_t *v,
-                                      const TreePrefix &t, int64_t L_max, int kb, int B, int Hq,
-                                      int Hkv, int D, float scale, int ctas, cudaStream_t s);
-int tree_max_drafts();
+                                      const TreePrefix &t, int64_t L_max, int B, int Hq, int Hkv,
+                                      int D, float scale, void *status, int ctas,
+                                      cudaStream_t s);
 size_t tree_dense_ws_bytes(int B, int N, int Hq, int Hkv, int D);
 size_t tree_sparse_ws_bytes(int B, int N, int Hq, int D);
 cudaError_t launch_tree_decode(const uint16_t *q, const uint16_t *k, const uint16_t *v,

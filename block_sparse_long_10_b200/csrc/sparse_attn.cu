@@ -32,9 +32,11 @@ constexpr int THREADS = WARPS * 32;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
-// TREE: a slice of one drafted token's selection over its committed prefix; entry
-// kb - 1 stands for the tokens after the last complete block.  All rows' stages, in one
-// row, are cut into equal runs, one per CTA; each row that a run meets leaves a part.
+// TREE: a slice of one drafted token's list: its selection over the committed prefix, the
+// tokens after the last complete block (one entry), then its chain of drafts, four tokens
+// an entry, gathered one by one like the others: nothing of another branch is read.  All
+// rows' stages, in one row, are cut into equal runs, one per CTA; each row that a run meets
+// leaves a part.
 enum Mode { PREFILL = 0, SPLIT = 1, TREE = 2 };
 
 // Prefill: 2-stage ring, 3 CTAs per SM (12 warps: the gather is latency-bound
@@ -57,8 +59,11 @@ struct Cfg {
     static constexpr int STAGE_K = KS * ROW;
     static constexpr int STAGE_BYTES = 2 * STAGE_K;   // K then V
     static constexpr int OFF_SEL = STAGES * STAGE_BYTES;
-    static constexpr int MAX_ENT = 1028;  // TREE: 1024 and the tail
+    static constexpr int MAX_ENT = 1024;
+    static constexpr int TREE_ENT = MAX_ENT + 4 + TREE_DRAFTS / 4;  // and tail and chain
+    static constexpr int OFF_CHAIN = OFF_SEL + TREE_ENT * 4;
     static constexpr int BYTES = OFF_SEL + MAX_ENT * 4;
+    static constexpr int TREE_BYTES = OFF_CHAIN + TREE_DRAFTS * 4;
     // merge area (aliases the stage ring once it has drained)
     static constexpr int MERGE_BYTES = WARPS * (D * 8 + 16) * 4;
     static_assert(MERGE_BYTES <= STAGES * STAGE_BYTES, "merge area");
@@ -85,12 +90,14 @@ struct Args {
     TreePrefix tree;         // TREE mode
 };
 
-// A CTA's run of stages over all live rows, nst stages each.  (32 bits: the rows number at
-// most 2^31 / 32, refused beyond; their stages would be 2^31 only with 100 GB of queries.)
+// A CTA's run of stages over all live rows, nst stages each and START that stand for what a
+// CTA spends on going over to another row (32 bits: the rows number at most 2^31 / 32,
+// refused beyond; their stages would be 2^31 only with 100 GB of queries.)
 struct TreeRun {
+    static constexpr int START = 3;
     int pos, hi, b, b0;  // b0: flat index of sequence b's first stage
     int64_t P;           // of the current row: committed tokens
-    int i, s0, n, nst;   // draft, first stage, stages
+    int i, s0, n, nst;   // draft, first stage, stages; of a row with its START
 
     QSA_DEVICE static int drafts(const TreePrefix &t, int b, int64_t Tk, int64_t &P) {
         const int64_t S = t.seqlens[b];
@@ -101,7 +108,7 @@ struct TreeRun {
     }
     // Whole warps; false: nothing for this CTA.
     QSA_DEVICE bool start(const TreePrefix &t, int B, int64_t Tk, int nst_, int lane) {
-        nst = nst_;
+        nst = nst_ + START;
         int total = 0, w0 = 0;
         int64_t skip;
         for (int j = 0; j < B; j += 32) {
@@ -135,18 +142,21 @@ struct TreeRun {
         }
     }
     QSA_DEVICE bool next(const TreePrefix &t, int64_t Tk) {
-        if (pos >= hi) return false;
-        int w = drafts(t, b, Tk, P) * nst;
-        while (pos >= b0 + w) {
-            b0 += w;
-            w = drafts(t, ++b, Tk, P) * nst;
+        while (pos < hi) {
+            int w = drafts(t, b, Tk, P) * nst;
+            while (pos >= b0 + w) {
+                b0 += w;
+                w = drafts(t, ++b, Tk, P) * nst;
+            }
+            i = (pos - b0) / nst;
+            const int at = pos - b0 - i * nst, len = min(hi - pos, nst - at);
+            pos += len;
+            if (at + len <= START) continue;
+            s0 = max(at - START, 0);
+            n = at + len - START - s0;
+            return true;
         }
-        const int at = pos - b0;
-        i = at / nst;
-        s0 = at - i * nst;
-        n = min(hi - pos, nst - s0);
-        pos += n;
-        return true;
+        return false;
     }
 };
 
@@ -158,6 +168,7 @@ __global__ void __launch_bounds__(THREADS, Ring<MODE>::CTAS) sparse_attn_kernel(
     constexpr int KSTEP = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
     int *s_blk = reinterpret_cast<int *>(smem + C::OFF_SEL);
+    int *s_chain = reinterpret_cast<int *>(smem + C::OFF_CHAIN);  // TREE: tokens, or -1
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int lr = lane >> 2, lc = lane & 3;
     const int g = warp / C::WPG, sub = warp % C::WPG;
@@ -190,6 +201,20 @@ __global__ void __launch_bounds__(THREADS, Ring<MODE>::CTAS) sparse_attn_kernel(
                 if (run.s0 == 0) a.tree.first[row * a.tree.stride] = blockIdx.x;
                 if (e1 == a.kb) a.tree.last[row * a.tree.stride] = blockIdx.x;
             }
+            // the chain, from the draft up: a parent must come before its child, any other
+            // value ends it
+            if (e1 > a.tree.kb + 1 && warp == WARPS - 1) {
+                const int32_t *parent = a.tree.parent + b * a.tree.N;
+                int len = 0;
+                for (int j = run.i; j >= 0; ++len) {
+                    if (lane == 0) s_chain[len] = (int)run.P + j;
+                    const int up = parent[j];
+                    const bool wrong = (uint32_t)(up + 1) > (uint32_t)j;
+                    if (wrong && j == run.i && lane == 0) record_status(a.status, QSA_ERR_DEVICE);
+                    j = wrong ? -1 : up;
+                }
+                for (len += lane; len < (a.kb - a.tree.kb - 1) * 4; len += 32) s_chain[len] = -1;
+            }
         } else {
             b = item / a.nsplit;
             row = b;
@@ -212,9 +237,11 @@ __global__ void __launch_bounds__(THREADS, Ring<MODE>::CTAS) sparse_attn_kernel(
                 const int64_t whole = (p + 1) / 4;
                 const int e = e0 + i;
                 int j = (int)whole;
-                if (e < a.kb - 1) {
-                    j = a.tree.sel[b * a.tree.sel_b + (row - b * a.tree.N) * a.tree.sel_n + e];
-                    if (j >= whole) j = -1;
+                if (e < a.tree.kb) {
+                    j = a.tree.sel[b * a.tree.sel_b + run.i * a.tree.sel_n + e];
+                    if (j < 0 || j >= whole) j = -1;
+                } else if (e > a.tree.kb) {
+                    j = a.tree.kb - 1 - e;  // -2, -3, ...: four of the chain
                 }
                 s_blk[i] = j;
                 continue;
@@ -257,8 +284,13 @@ __global__ void __launch_bounds__(THREADS, Ring<MODE>::CTAS) sparse_attn_kernel(
                     const int r = k / MR;                    // token of the block
                     const int ch = li + TPB * (k % MR);      // 16-byte chunk of its key row
                     const int kk = bi * 4 + r;
-                    const bool ok = j >= 0 && u0 + r <= p;
-                    const int64_t off = ok ? (u0 + r) * (HKV * D) + ch * 8 : 0;
+                    int64_t u = u0 + r;
+                    bool ok = j >= 0 && u <= p;
+                    if (MODE == TREE && j < -1) {
+                        u = s_chain[(-2 - j) * 4 + r];
+                        ok = u >= 0;
+                    }
+                    const int64_t off = ok ? u * (HKV * D) + ch * 8 : 0;
                     // chunk ch of the key row = head ch / (D/8), dim chunk ch % (D/8)
                     const int hh = ch / (D / 8), dc = ch % (D / 8);
                     const int dst = kk * C::ROW + hh * D * 2 + ((dc ^ (kk & 7)) * 16);
@@ -304,7 +336,8 @@ __global__ void __launch_bounds__(THREADS, Ring<MODE>::CTAS) sparse_attn_kernel(
                 const int kk = sub * 16 + lr + hrow * 8;
                 const int ent = s * C::NBS + (kk >> 2);
                 const int j = ent < n_ent ? s_blk[ent] : -1;
-                const bool ok = j >= 0 && (int64_t)j * 4 + (kk & 3) <= p;
+                bool ok = j >= 0 && (int64_t)j * 4 + (kk & 3) <= p;
+                if (MODE == TREE && j < -1) ok = s_chain[(-2 - j) * 4 + (kk & 3)] >= 0;
                 x[hrow * 2 + 0] = ok ? sacc[hrow * 2 + 0] * a.scale_log2 : -INFINITY;
                 x[hrow * 2 + 1] = ok ? sacc[hrow * 2 + 1] * a.scale_log2 : -INFINITY;
             }
@@ -445,10 +478,11 @@ template <int D, int G, int HKV, int MODE>
 static cudaError_t launch_sat(const Args &a, int grid, cudaStream_t s) {
     using C = Cfg<D, HKV, Ring<MODE>::STAGES>;
     auto kern = sparse_attn_kernel<D, G, HKV, MODE>;
-    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), C::BYTES);
+    constexpr int bytes = MODE == TREE ? C::TREE_BYTES : C::BYTES;
+    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), bytes);
     if (e != cudaSuccess) return e;
     if (a.total_items == 0) return cudaSuccess;
-    return launch_dependent(kern, dim3(grid), dim3(THREADS), (size_t)C::BYTES, s, a);
+    return launch_dependent(kern, dim3(grid), dim3(THREADS), (size_t)bytes, s, a);
 }
 
 template <int MODE>
@@ -512,11 +546,13 @@ cudaError_t launch_split_decode(const uint16_t *q, const uint16_t *k, const uint
 int tree_sparse_ctas(int num_sms) { return num_sms * sat::Ring<sat::TREE>::CTAS; }
 
 cudaError_t launch_tree_sparse_prefix(const uint16_t *q, const uint16_t *k, const uint16_t *v,
-                                      const TreePrefix &t, int64_t L_max, int kb, int B, int Hq,
-                                      int Hkv, int D, float scale, int ctas, cudaStream_t s) {
+                                      const TreePrefix &t, int64_t L_max, int B, int Hq, int Hkv,
+                                      int D, float scale, void *status, int ctas,
+                                      cudaStream_t s) {
     sat::Args a{};
     a.q = q; a.k = k; a.v = v; a.seqlens = t.seqlens; a.B = B; a.Tk = L_max; a.Hq = Hq;
-    a.kb = kb + 1; a.scale_log2 = scale * sat::LOG2E; a.tree = t;
+    a.kb = t.kb + 1 + (t.N + 3) / 4; a.scale_log2 = scale * sat::LOG2E; a.tree = t;
+    a.status = status;
     a.total_items = (int64_t)B * t.N;
     return sat::dispatch<sat::TREE>(a, D, Hq / Hkv, Hkv, ctas, s);
 }

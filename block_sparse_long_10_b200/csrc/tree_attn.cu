@@ -12,9 +12,8 @@
 // lie behind the prefix in the same tiles: two matrix products (tree_dense_kernel) with a
 // mask of ancestors, in which values of drafts that are not finite count as zeros; the
 // merge adds them to the rows whose chains they are in.  Selections differ from row to row:
-// they are gathered row by row (sparse_attn.cu), and the merge walks the chains, token by
-// token, in fp32.  All parts of a row are (max, sum, O) in base 2 and meet in
-// tree_merge_kernel.
+// they and the chains are gathered row by row (sparse_attn.cu).  All parts of a row are
+// (max, sum, O) in base 2 and meet in tree_merge_kernel.
 #include "qsa_common.cuh"
 #include "qsa_launch.h"
 #include "sm100.cuh"
@@ -23,7 +22,7 @@ namespace qsa {
 
 namespace tree {
 
-constexpr int MAX_N = 256;  // drafts per sequence
+constexpr int MAX_N = TREE_DRAFTS;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
@@ -712,9 +711,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == SOFT / 32 + 1) sm100::tmem_dealloc(tmem, 512);
 }
 
-// --------------------------------------------------------- chains and merge --
-// One query head against single tokens: groups of 8 lanes take a token each; a lane
-// holds E = D / 8 dims.  Running (max, sum, O) per group, in base 2.
+// ------------------------------------------------------------------ merge --
+// A query head in a group of 8 lanes, E = D / 8 dims a lane: running (max, sum, O).
 template <int D>
 struct Row {
     static constexpr int E = D / 8;
@@ -770,14 +768,6 @@ struct Row {
         x += __shfl_xor_sync(0xffffffffu, x, 4);
         return x * scale_log2;
     }
-    // a token's cache rows; `on` false: the group sits out (all lanes call)
-    QSA_DEVICE void token(const Raw &k, const Raw &v, bool on, float scale_log2) {
-        const float x = score(k, scale_log2);
-        if (!on) return;
-        float f[E];
-        v.get(f);
-        join(x, 1.f, f);
-    }
     // of a token that is in m and l already, the values that are not finite
     QSA_DEVICE void patch(const Raw &k, const Raw &v, float scale_log2) {
         const float p = fast_exp2(score(k, scale_log2) - (m == -INFINITY ? 0.f : m));
@@ -816,7 +806,6 @@ __global__ void __launch_bounds__(256, 3) tree_merge_kernel(const Args a) {
     const int h = W > 1 ? (int)blockIdx.y : (int)(blockIdx.y * (blockDim.x >> 5)) + warp;
     const int grp = (W > 1 ? warp * 4 : 0) + (lane >> 3);
     const Seq sq = a.lens.at(b);
-    const int32_t *parent = a.parent + b * a.N;
     if (sq.bad) {
         if (i == 0 && h == 0 && lane == 0) record_status(a.status, QSA_ERR_DEVICE);
     } else if (i >= sq.n) {
@@ -826,40 +815,6 @@ __global__ void __launch_bounds__(256, 3) tree_merge_kernel(const Args a) {
     r.start(a.q + (row * a.Hq + h) * D, li);
     const int64_t tok = (int64_t)a.Hkv * D;
     const int64_t base = (b * a.lens.L_max + sq.P) * tok + (h >> a.lg) * D + li * E;
-    // A parent must come before its child; any other value ends the chain.
-    auto above = [&](int j) {
-        const int p = parent[j];
-        const bool wrong = p < -1 || p >= j;
-        if (wrong && j == i && lane == 0) record_status(a.status, QSA_ERR_DEVICE);
-        return wrong ? -1 : p;
-    };
-    if (SPARSE && !sq.bad) {
-        int j = i;
-        // the next 4 W drafts of the chain: this group's, or -1
-        auto walk = [&]() {
-            int mine = -1;
-            for (int s = 0; s < 4 * W && j >= 0; ++s, j = above(j))
-                if (s == grp) mine = j;
-            return mine;
-        };
-        int mine = walk();
-        typename Row<D>::Raw k, v;
-        const int64_t at0 = base + (mine < 0 ? 0 : mine) * tok;
-        if (mine >= 0) {
-            k.load(a.k + at0);
-            v.load(a.v + at0);
-        }
-        while (__any_sync(0xffffffffu, mine >= 0)) {
-            const typename Row<D>::Raw k1 = k, v1 = v;
-            const bool on = mine >= 0;
-            mine = walk();
-            if (mine >= 0) {
-                k.load(a.k + base + mine * tok);
-                v.load(a.v + base + mine * tok);
-            }
-            r.token(k1, v1, on, a.scale_log2);
-        }
-    }
     griddep_wait();  // the prefix kernel's parts
     int64_t x0 = 0;
     int parts = 0;
@@ -928,11 +883,13 @@ __global__ void __launch_bounds__(256, 3) tree_merge_kernel(const Args a) {
     }
     // what was cleared in the chain's values, all groups the same token
     if (!SPARSE && patch)
-        for (int j = i; j >= 0; j = above(j)) {
+        for (int j = i; j >= 0;) {
             typename Row<D>::Raw k, v;
             k.load(a.k + base + j * tok);
             v.load(a.v + base + j * tok);
             r.patch(k, v, a.scale_log2);
+            const int p = a.parent[b * a.N + j];
+            j = (uint32_t)(p + 1) > (uint32_t)j ? -1 : p;
         }
     if (lane < 8) {
         const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
@@ -998,8 +955,6 @@ cudaError_t run_merge(const Args &a, cudaStream_t s) {
 
 }  // namespace tree
 
-int tree_max_drafts() { return tree::MAX_N; }
-
 size_t tree_dense_ws_bytes(int B, int N, int Hq, int Hkv, int D) {
     return tree::dense_ws(B, N, Hkv, Hq / Hkv, D).bytes;
 }
@@ -1030,9 +985,9 @@ cudaError_t launch_tree_decode(const uint16_t *q, const uint16_t *k, const uint1
     if (sel) {
         a.units = 1;
         a.rows = Hq;
-        const TreePrefix t{seqlens, n_draft, N, sel, sel_b, sel_n, a.part, a.ml, &a.info->first, &a.info->last,
+        const TreePrefix t{seqlens, n_draft, parent, N, sel, sel_b, sel_n, kb, a.part, a.ml, &a.info->first, &a.info->last,
                            sizeof(tree::UnitInfo) / 4};
-        e = launch_tree_sparse_prefix(q, k, v, t, L_max, kb, B, Hq, Hkv, D, scale,
+        e = launch_tree_sparse_prefix(q, k, v, t, L_max, B, Hq, Hkv, D, scale, ws,
                                       tree_sparse_ctas(sms), s);
     } else {
         a.units = tree::unit_count(N, a.G);
