@@ -111,7 +111,7 @@ struct Cfg {
     static constexpr int SLOTS = FIT > 8 ? 8 : FIT;
     static constexpr int OFF_BAR = OFF_RING + SLOTS * TILE;
     static constexpr int BYTES = 1024 + OFF_BAR + 512;
-    static_assert((3 * SLOTS + 6) * 8 + 16 <= 512, "barriers");
+    static_assert((4 * SLOTS + 6) * 8 + 16 <= 512, "barriers");
     static_assert(NT == 2 || 2 * 128 * 8 <= TILE, "the streams' sums fit in the query tile");
     // TMEM columns
     static constexpr int O_COL = 256;
@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR), *empty = full + SL;
-    uint64_t *clean = empty + SL;  // values of drafts are
+    uint64_t *dfull = empty + SL, *clean = dfull + SL;  // drafts' values have come; are clean
     uint64_t *sfull = clean + SL, *pready = sfull + 2, *odone = pready + 2, *qready = odone + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(qready + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -450,6 +450,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = 0; i < SL; ++i) {
             sm100::mbar_init(&full[i], 1);
             sm100::mbar_init(&empty[i], 1);
+            sm100::mbar_init(&dfull[i], 1);
             sm100::mbar_init(&clean[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -476,32 +477,40 @@ __global__ void __launch_bounds__(THREADS, 1)
         // ------------------------------------------------------ producer --
         if (lane == 0) {
             sm100::prefetch_tensormap(&tm);
-            uint32_t it = 0;
+            uint32_t it = 0, drafts = 0;
             bool dead = false;
-            auto put = [&](int cache, int64_t tile) {
+            auto put = [&](int cache, int64_t tile, bool cleaned) {
                 const uint32_t slot = it % SL;
                 if (dead || !wait(&empty[slot], (it / SL) + 1)) {
                     dead = true;
                     return;
                 }
-                sm100::mbar_arrive_expect_tx(&full[slot], C::TILE);
+                // values that are cleaned first complete a barrier of their own
+                uint64_t *bar = &full[slot];
+                if (cleaned) {
+                    sm100::mbar_arrive(bar);
+                    bar = &dfull[drafts++ % SL];
+                }
+                sm100::mbar_arrive_expect_tx(bar, C::TILE);
 #pragma unroll
                 for (int at = 0; at < D / 64; ++at)
                     sm100::tma_load_4d(ring + slot * C::TILE + at * ATOM, &tm, sg.g * D + at * 64,
-                                       (int32_t)(tile * KT), (int32_t)sg.b, cache, &full[slot]);
+                                       (int32_t)(tile * KT), (int32_t)sg.b, cache, bar);
                 ++it;
             };
             while (walk.next(a, sg)) {
-                put(a.k_at, sg.t0);
+                put(a.k_at, sg.t0, false);
                 for (int j = 0; j < sg.n; ++j) {
-                    if (NT == 1 && j + 1 < sg.n) put(a.k_at, sg.t0 + j + 1);
-                    put(a.v_at, sg.t0 + j);
-                    if (NT == 2 && j + 1 < sg.n) put(a.k_at, sg.t0 + j + 1);
+                    if (NT == 1 && j + 1 < sg.n) put(a.k_at, sg.t0 + j + 1, false);
+                    put(a.v_at, sg.t0 + j, has_drafts(sg, j));
+                    if (NT == 2 && j + 1 < sg.n) put(a.k_at, sg.t0 + j + 1, false);
                 }
             }
             // no copy may land after the CTA has gone
             for (uint32_t i = it > SL ? it - SL : 0; i < it; ++i)
                 sm100::mbar_wait_for(&full[i % SL], (i / SL) & 1, 100000000ull);
+            for (uint32_t i = drafts > SL ? drafts - SL : 0; i < drafts; ++i)
+                sm100::mbar_wait_for(&dfull[i % SL], (i / SL) & 1, 100000000ull);
         }
     } else if (warp == SOFT / 32 + 1) {
         // ----------------------------------------------------------- MMA --
@@ -537,11 +546,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const uint32_t idx = ring_v<NT>(base, NT == 2 ? t >> 1 : t, n), slot = idx % SL;
                 wait(&pready[s], done[s]++);
                 if (NT == 1 || s == 0) {
-                    if (has_drafts(sg, NT == 2 ? t >> 1 : t)) {
-                        wait(&clean[slot], cleaned >> slot);
-                        cleaned ^= 1u << slot;
-                    }
                     wait(&full[slot], idx / SL);
+                    if (has_drafts(sg, NT == 2 ? t >> 1 : t)) {
+                        wait(&clean[cleaned % SL], cleaned / SL);
+                        ++cleaned;
+                    }
                 }
                 sm100::tc_fence_after();
                 const uint64_t va = sm100::smem_desc_mnmajor(ring + slot * C::TILE, ATOM);
@@ -561,16 +570,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp == SOFT / 32 + 2) {
         // ---------------------------------------------------------- clean --
         // V rows of drafts, before they meet zeros: no infinity, no NaN; and none at all
-        // behind the drafts.  (A slot is used again only after its product, so the slots'
-        // barriers are never two phases ahead.)
-        uint32_t base = 0;
+        // behind the drafts.  Such tiles have barriers of their own, in their own order: a
+        // wait for a ring slot's parity passes if the phase before has not ended either, and
+        // this warp does not wait for the others' phases.  (No more than SLOTS are on their
+        // way, so no barrier is a phase ahead.)
+        uint32_t base = 0, drafts = 0;
         while (walk.next(a, sg)) {
             const int64_t u = (sg.b * a.Hkv + sg.g) * a.units + sg.qt;
             for (int j = 0; j < sg.n; ++j) {
                 if (!has_drafts(sg, j)) continue;
                 const int64_t pl = sg.P - (sg.t0 + j) * KT, sl = pl + sg.nd;
-                const uint32_t idx = ring_v<NT>(base, j, sg.n), slot = idx % SL;
-                wait(&full[slot], idx / SL);
+                const uint32_t slot = ring_v<NT>(base, j, sg.n) % SL, x = drafts % SL;
+                wait(&dfull[x], drafts / SL);
+                ++drafts;
                 uint8_t *vt = sm + C::OFF_RING + slot * C::TILE;
                 const bool some = clean_rows<D>(vt, pl > 0 ? (int)pl : 0, sl < KT ? (int)sl : KT,
                                                 lane);
@@ -578,7 +590,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const bool any = __any_sync(0xffffffffu, some);
                 if (lane == 0) {
                     a.info[u].cleared[sg.t0 + j - sg.P / KT] = any;
-                    sm100::mbar_arrive(&clean[slot]);
+                    sm100::mbar_arrive(&clean[x]);
                 }
             }
             base += 2 * sg.n;

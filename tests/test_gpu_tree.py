@@ -219,6 +219,27 @@ def test_scales(scale):
         _check(x, o, lse, prefix, drafts, sel, scale=scale)
 
 
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,top", [(40, 5, 8, 4, 128, 2600), (24, 40, 32, 4, 128, 2500),
+                                              (60, 3, 2, 2, 64, 5000), (16, 200, 8, 1, 64, 3000)])
+def test_long_runs(B, N, Hq, Hkv, D, top):
+    """More tiles (and stages of selections) than SMs by far: each SM's ring of copies wraps
+    several times, goes over from sequence to sequence, and meets drafts on the way."""
+    prefix = [top - (37 * b) % 1111 for b in range(B)]
+    drafts = [N - (b % 3) * (N // 4) for b in range(B)]
+    x = _make(B, N, Hq, Hkv, D, prefix, drafts, seed=31)
+    sel = _sel(prefix, N, 512, 32)
+    for s in (None, sel):
+        first = _run(x, s, 2048)
+        assert qsa.qsa_check_device_status(first[2]) == 0
+        some = sorted({0, 1, B // 2, B - 1})
+        part = {n: t[some] for n, t in x.items()}
+        _check(part, first[0][some], first[1][some], [prefix[b] for b in some],
+               [drafts[b] for b in some], None if s is None else s[some], rows={0, N // 2, N - 1})
+        for _ in range(5):  # all rows, whatever the timing
+            again = _run(x, s, 2048, ws=first[2])
+            assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+
+
 def test_growing_logits_move_the_running_maximum():
     """Keys that grow along the cache: the maximum moves in every tile."""
     prefix, drafts = [1500], [4]
