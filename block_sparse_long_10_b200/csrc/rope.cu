@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const RopeArgs a) {
     const Lane<VEC, HALF> L(lane, a.rot);
     double tf[VEC];
     load_turns<VEC>(a.freq, L.f0, L.turns, tf);
-    const int64_t per_block = THREADS / a.lanes;
+    const int64_t per_block = blockDim.x / a.lanes;
     const int64_t items = a.n_tok * a.n_hg;
     for (int64_t it = blockIdx.x * per_block + threadIdx.x / a.lanes; it < items;
          it += gridDim.x * per_block) {
@@ -403,7 +403,7 @@ struct Batches {
 
 // Turns per position of the frequency table, p * freq / 2 pi, once per block.
 QSA_DEVICE void load_table(const double *freq, int rot, double *s_tf) {
-    for (int i = threadIdx.x; i < rot / 2; i += THREADS) s_tf[i] = freq[i] * INV_2PI;
+    for (int i = threadIdx.x; i < rot / 2; i += blockDim.x) s_tf[i] = freq[i] * INV_2PI;
     __syncthreads();
 }
 
@@ -414,6 +414,13 @@ QSA_DEVICE void table_angles(int64_t p, const double *s_tf, int f0, bool turns, 
 #pragma unroll
     for (int e = 0; e < VEC; ++e) tf[e] = turns ? s_tf[f0 + e] : 0.0;
     angles<VEC>(p, tf, turns, mscale, sign, c, s);
+}
+
+// Asks for a sector of an array (or of none) and does not wait for it.
+QSA_DEVICE void warm(const float *p, int i) {
+    if (p)
+        asm volatile("{\n\t.reg .b32 x;\n\tld.global.ca.b32 x, [%0];\n\t}\n" ::"l"(p + i)
+                     : "memory");
 }
 
 struct NormArgs {
@@ -445,9 +452,14 @@ __global__ void __launch_bounds__(THREADS, NORM_CTAS) norm_rope_kernel(const Nor
     __shared__ double s_tf[128];
     const int lane = threadIdx.x % LANES;
     const Lane<VEC, HALF> L(lane, a.rot);
-    constexpr int per_block = THREADS / LANES;
+    const int per_block = blockDim.x / LANES;
     const int64_t stride = (int64_t)gridDim.x * per_block;
     const int64_t items = a.n_tok * a.n_hg;
+    // the weights into L1, for when the first rows have come
+    for (int i = threadIdx.x; i < D / 8; i += blockDim.x) {
+        warm(a.w[0], i * 8);
+        warm(a.w[1], i * 8);
+    }
     // whole warps stay in the loop (the sums are shuffles): as long as their first group
     const int64_t wfirst = (int64_t)blockIdx.x * per_block + (threadIdx.x & ~31) / LANES;
     const int steps = wfirst < items ? (int)((items - wfirst + stride - 1) / stride) * a.hpb : 0;
@@ -830,8 +842,16 @@ int batches_per_item(int64_t n_tok, int batches, int lanes, int num_sms) {
     return n_tok * lanes < (int64_t)num_sms * 512 ? 1 : batches < 3 ? batches : 3;
 }
 
-int grid_of(int64_t items, int lanes, int num_sms, int per_sm) {
-    const int64_t per_block = THREADS / lanes;
+// Threads of a block: 256, or fewer while that leaves SMs without one (64 sequences' decode
+// step: 4.1 us with 64 threads a block, 5.4 with 256).
+int block_of(int64_t items, int lanes, int num_sms) {
+    int t = THREADS;
+    while (t > 64 && items * lanes < (int64_t)num_sms * t) t /= 2;
+    return t;
+}
+
+int grid_of(int64_t items, int lanes, int num_sms, int per_sm, int threads = THREADS) {
+    const int64_t per_block = threads / lanes;
     const int64_t need = (items + per_block - 1) / per_block;
     const int64_t cap = (int64_t)num_sms * per_sm;
     return (int)(need < cap ? (need > 0 ? need : 1) : cap);
@@ -853,28 +873,32 @@ void grad_grid(int64_t n_tok, int Hq, int Hkv, int D, int num_sms, int *nq, int 
 }
 
 template <typename T, int VEC>
-cudaError_t run_rope(const RopeArgs &a, bool half, int grid, cudaStream_t s) {
+cudaError_t run_rope(const RopeArgs &a, bool half, int grid, int threads, cudaStream_t s) {
     if (half)
-        rope_kernel<T, VEC, true><<<grid, THREADS, 0, s>>>(a);
+        rope_kernel<T, VEC, true><<<grid, threads, 0, s>>>(a);
     else
-        rope_kernel<T, VEC, false><<<grid, THREADS, 0, s>>>(a);
+        rope_kernel<T, VEC, false><<<grid, threads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
 template <int D, int VEC, bool HALF>
-cudaError_t run_norm(const NormArgs &a, int grid, cudaStream_t s) {
+cudaError_t run_norm(const NormArgs &a, int grid, int threads, cudaStream_t s) {
     constexpr int bytes = 2 * VEC * 2 * NORM_ROWS * NORM_STAGES * THREADS;
     auto kern = norm_rope_kernel<D, VEC, HALF>;
     const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), bytes);
     if (e != cudaSuccess) return e;
-    kern<<<grid, THREADS, bytes, s>>>(a);
+    kern<<<grid, threads, bytes, s>>>(a);
     return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t run_norm(const NormArgs &a, int vec, bool half, int grid, cudaStream_t s) {
-    if (vec == 8) return half ? run_norm<D, 8, true>(a, grid, s) : run_norm<D, 8, false>(a, grid, s);
-    return half ? run_norm<D, 4, true>(a, grid, s) : run_norm<D, 4, false>(a, grid, s);
+cudaError_t run_norm(const NormArgs &a, int vec, bool half, int num_sms, cudaStream_t s) {
+    const int64_t items = a.n_tok * a.n_hg;
+    const int lanes = D / (2 * vec), t = block_of(items, lanes, num_sms);
+    const int grid = grid_of(items, lanes, num_sms, NORM_CTAS, t);
+    if (vec == 8)
+        return half ? run_norm<D, 8, true>(a, grid, t, s) : run_norm<D, 8, false>(a, grid, t, s);
+    return half ? run_norm<D, 4, true>(a, grid, t, s) : run_norm<D, 4, false>(a, grid, t, s);
 }
 
 template <int D, bool HALF, typename TD, typename TX>
@@ -918,10 +942,12 @@ cudaError_t launch_rope(const void *x, int64_t xs, void *y, int64_t ys, bool fp3
     a.n_hg = (H + a.hpg - 1) / a.hpg;
     a.freq = freq; a.mscale = mscale; a.sign = transpose ? -1.f : 1.f;
     a.pos = Pos{pos, pos0};
-    const int grid = grid_of(a.n_tok * a.n_hg, a.lanes, num_sms, 8);
-    if (fp32) return run_rope<float, 4>(a, half, grid, s);
-    return vec == 8 ? run_rope<uint16_t, 8>(a, half, grid, s)
-                    : run_rope<uint16_t, 4>(a, half, grid, s);
+    const int64_t items = a.n_tok * a.n_hg;
+    const int t = block_of(items, a.lanes, num_sms);
+    const int grid = grid_of(items, a.lanes, num_sms, 8, t);
+    if (fp32) return run_rope<float, 4>(a, half, grid, t, s);
+    return vec == 8 ? run_rope<uint16_t, 8>(a, half, grid, t, s)
+                    : run_rope<uint16_t, 4>(a, half, grid, t, s);
 }
 
 cudaError_t launch_norm_rope(const uint16_t *q, int64_t qs, const uint16_t *k, int64_t ks,
@@ -947,11 +973,10 @@ cudaError_t launch_norm_rope(const uint16_t *q, int64_t qs, const uint16_t *k, i
     a.hpb = batches_per_item(a.n_tok, a.batches, lanes, num_sms);
     a.n_hg = (a.batches + a.hpb - 1) / a.hpb;
     a.eps = eps; a.freq = freq; a.mscale = mscale; a.pos = Pos{pos, pos0}; a.status = status;
-    const int grid = grid_of(a.n_tok * a.n_hg, lanes, num_sms, NORM_CTAS);
-    return D == 32   ? run_norm<32>(a, vec, half, grid, s)
-           : D == 64 ? run_norm<64>(a, vec, half, grid, s)
-           : D == 128 ? run_norm<128>(a, vec, half, grid, s)
-                      : run_norm<256>(a, vec, half, grid, s);
+    return D == 32    ? run_norm<32>(a, vec, half, num_sms, s)
+           : D == 64  ? run_norm<64>(a, vec, half, num_sms, s)
+           : D == 128 ? run_norm<128>(a, vec, half, num_sms, s)
+                      : run_norm<256>(a, vec, half, num_sms, s);
 }
 
 // The grid depends on the device, so the workspace is sized for the largest one.
