@@ -825,11 +825,13 @@ __global__ void __launch_bounds__(1024)
 // (rot a multiple of 16), else 8-byte ones; fp32 rows always take 16 bytes.
 int pick_vec(int rot) { return rot % 16 == 0 ? 8 : 4; }
 
-// Heads per item of the plain rotation: all of a token's rows share one set of angles, but
-// a small batch is spread over more lanes first.
+// Heads per item of the plain rotation: a token's heads share one set of angles, but at most
+// the ROWS whose loads go together (2 x 4099 tokens of 16 heads of 128 in fp32: 23.8 us; 25.2
+// with 8), and a small batch is spread over more lanes first.  (Through the ring below it
+// took 37 us: without the norms' arithmetic there is nothing for a ring to hide.)
 int heads_per_item(int64_t n_tok, int rows, int lanes, int num_sms) {
     const int64_t want = (int64_t)num_sms * 1024 / lanes;  // groups that fill the GPU
-    int hpg = rows;
+    int hpg = rows < ROWS ? rows : ROWS;
     while (hpg > 1 && n_tok * ((rows + hpg - 1) / hpg) < want) hpg = (hpg + 1) / 2;
     return hpg;
 }
