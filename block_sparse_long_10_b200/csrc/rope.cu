@@ -25,29 +25,16 @@ namespace qsa {
 namespace rope {
 
 constexpr int THREADS = 256;
-constexpr int ROWS = 4;  // head rows whose loads are issued together
+// The plain rotation: vectors of 4 (with 8, in bf16, 98 registers a thread left two blocks an SM:
+// 8 x 900 tokens of 16 heads of 128 15.0 us, with 4 13.0), and head rows whose loads are issued
+// together.
+constexpr int ROPE_VEC = 4;
+template <typename T>
+constexpr int ROPE_ROWS = sizeof(T) == 4 ? 2 : 4;
 constexpr double INV_2PI = 0.15915494309189533576888376337251;
 
 template <typename T, int VEC>
 struct Raw;
-template <>
-struct Raw<uint16_t, 8> {
-    uint4 v;
-    QSA_DEVICE void load(const uint16_t *p) { v = *reinterpret_cast<const uint4 *>(p); }
-    QSA_DEVICE void store(uint16_t *p) const { *reinterpret_cast<uint4 *>(p) = v; }
-    QSA_DEVICE void get(float (&f)[8]) const {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = bf16_lo(w[i]);
-            f[2 * i + 1] = bf16_hi(w[i]);
-        }
-    }
-    QSA_DEVICE void set(const float (&f)[8]) {
-        v = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                       pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-    }
-};
 template <>
 struct Raw<uint16_t, 4> {
     uint2 v;
@@ -185,8 +172,9 @@ struct RopeArgs {
     Pos pos;
 };
 
-template <typename T, int VEC, bool HALF>
+template <typename T, bool HALF>
 __global__ void __launch_bounds__(THREADS) rope_kernel(const RopeArgs a) {
+    constexpr int VEC = ROPE_VEC, ROWS = ROPE_ROWS<T>;
     const int lane = threadIdx.x % a.lanes;
     const Lane<VEC, HALF> L(lane, a.rot);
     double tf[VEC];
@@ -826,12 +814,12 @@ __global__ void __launch_bounds__(1024)
 int pick_vec(int rot) { return rot % 16 == 0 ? 8 : 4; }
 
 // Heads per item of the plain rotation: a token's heads share one set of angles, but at most
-// the ROWS whose loads go together (2 x 4099 tokens of 16 heads of 128 in fp32: 23.8 us; 25.2
-// with 8), and a small batch is spread over more lanes first.  (Through the ring below it
-// took 37 us: without the norms' arithmetic there is nothing for a ring to hide.)
-int heads_per_item(int64_t n_tok, int rows, int lanes, int num_sms) {
+// `most` (2 x 4099 tokens of 16 heads of 128 in fp32: 23.3 us with 2, 23.7 with 4, 25.2 with
+// 8), and a small batch is spread over more lanes first.  (Through the ring below it took
+// 37 us: without the norms' arithmetic there is nothing for a ring to hide.)
+int heads_per_item(int64_t n_tok, int rows, int most, int lanes, int num_sms) {
     const int64_t want = (int64_t)num_sms * 1024 / lanes;  // groups that fill the GPU
-    int hpg = rows < ROWS ? rows : ROWS;
+    int hpg = rows < most ? rows : most;
     while (hpg > 1 && n_tok * ((rows + hpg - 1) / hpg) < want) hpg = (hpg + 1) / 2;
     return hpg;
 }
@@ -874,12 +862,12 @@ void grad_grid(int64_t n_tok, int Hq, int Hkv, int D, int num_sms, int *nq, int 
     *nk = (int)(k < 1 ? 1 : k);
 }
 
-template <typename T, int VEC>
+template <typename T>
 cudaError_t run_rope(const RopeArgs &a, bool half, int grid, int threads, cudaStream_t s) {
     if (half)
-        rope_kernel<T, VEC, true><<<grid, threads, 0, s>>>(a);
+        rope_kernel<T, true><<<grid, threads, 0, s>>>(a);
     else
-        rope_kernel<T, VEC, false><<<grid, threads, 0, s>>>(a);
+        rope_kernel<T, false><<<grid, threads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -936,20 +924,18 @@ cudaError_t launch_rope(const void *x, int64_t xs, void *y, int64_t ys, bool fp3
                         float mscale, bool transpose, const int64_t *pos, const int64_t *pos0,
                         int num_sms, cudaStream_t s) {
     using namespace rope;
-    const int vec = fp32 ? 4 : pick_vec(rot);
     RopeArgs a{};
     a.x = x; a.y = y; a.xs = xs; a.ys = ys; a.T = T; a.n_tok = (int64_t)B * T;
-    a.H = H; a.D = D; a.rot = rot; a.lanes = D / (2 * vec);
-    a.hpg = heads_per_item(a.n_tok, H, a.lanes, num_sms);
+    a.H = H; a.D = D; a.rot = rot; a.lanes = D / (2 * ROPE_VEC);
+    a.hpg = heads_per_item(a.n_tok, H, fp32 ? ROPE_ROWS<float> : ROPE_ROWS<uint16_t>, a.lanes,
+                           num_sms);
     a.n_hg = (H + a.hpg - 1) / a.hpg;
     a.freq = freq; a.mscale = mscale; a.sign = transpose ? -1.f : 1.f;
     a.pos = Pos{pos, pos0};
     const int64_t items = a.n_tok * a.n_hg;
     const int t = block_of(items, a.lanes, num_sms);
     const int grid = grid_of(items, a.lanes, num_sms, 8, t);
-    if (fp32) return run_rope<float, 4>(a, half, grid, t, s);
-    return vec == 8 ? run_rope<uint16_t, 8>(a, half, grid, t, s)
-                    : run_rope<uint16_t, 4>(a, half, grid, t, s);
+    return fp32 ? run_rope<float>(a, half, grid, t, s) : run_rope<uint16_t>(a, half, grid, t, s);
 }
 
 cudaError_t launch_norm_rope(const uint16_t *q, int64_t qs, const uint16_t *k, int64_t ks,
