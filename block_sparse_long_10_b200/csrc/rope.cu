@@ -824,12 +824,22 @@ int heads_per_item(int64_t n_tok, int rows, int most, int lanes, int num_sms) {
     return hpg;
 }
 
-// Batches of rows per item: three, which share one set of angles, or one where there are
-// too few tokens for one wave of groups (512 threads an SM).  Whole tokens leave the last
-// wave half empty: at 32K tokens of 6 batches 65 us with 6, 61 with 3, 65 with 2 (more
-// angles); backward of 8 batches 143 us with 8, 138 with 4, 134 with 3.
-int batches_per_item(int64_t n_tok, int batches, int lanes, int num_sms) {
-    return n_tok * lanes < (int64_t)num_sms * 512 ? 1 : batches < 3 ? batches : 3;
+// Batches of rows per item, up to three, which share one set of angles: what makes the fewest
+// rounds of the resident groups, each as long as its batches and the angles (`angles`, in
+// batches).  32K tokens of 6 batches: 61 us with 3, 65 with 2 (more angles) and 65 with all 6
+// (a last round that is half empty); 4000 tokens 13.7 us with 3, 16.5 with 1.
+int batches_per_item(int64_t n_tok, int batches, int64_t groups, double angles) {
+    int best = 1;
+    double least = 0;
+    for (int n = 1; n <= 3 && n <= batches; ++n) {
+        const int64_t items = n_tok * ((batches + n - 1) / n);
+        const double cost = (double)((items + groups - 1) / groups) * (n + angles);
+        if (n == 1 || cost < least) {
+            best = n;
+            least = cost;
+        }
+    }
+    return best;
 }
 
 // Threads of a block: 256, or fewer while that leaves SMs without one (64 sequences' decode
@@ -958,7 +968,8 @@ cudaError_t launch_norm_rope(const uint16_t *q, int64_t qs, const uint16_t *k, i
     a.first[2] = a.first[1] + bk;
     a.batches = a.first[2] + (v ? bk : 0);
     a.slot = slot; a.L = L; a.T = T; a.n_tok = (int64_t)B * T; a.rot = rot;
-    a.hpb = batches_per_item(a.n_tok, a.batches, lanes, num_sms);
+    a.hpb = batches_per_item(a.n_tok, a.batches, (int64_t)num_sms * NORM_CTAS * THREADS / lanes,
+                             0.9);
     a.n_hg = (a.batches + a.hpb - 1) / a.hpb;
     a.eps = eps; a.freq = freq; a.mscale = mscale; a.pos = Pos{pos, pos0}; a.status = status;
     return D == 32    ? run_norm<32>(a, vec, half, num_sms, s)
@@ -988,16 +999,16 @@ cudaError_t launch_norm_rope_grad(const void *d_q, const void *d_k, bool d_fp32,
     a.T = T; a.n_tok = (int64_t)B * T; a.rot = rot;
     a.eps = eps; a.freq = freq; a.mscale = mscale; a.pos = Pos{pos, pos0};
     const int sms = num_sms < 160 ? num_sms : 160;
-    auto side = [&](const void *dy, const uint16_t *x, int64_t xs, void *dx, const float *w,
-                    int H) {
-        const int n = (H + GRAD_ROWS - 1) / GRAD_ROWS;
-        const int hpb = batches_per_item(a.n_tok, n, lanes, sms);
-        return Side{dy, x, xs, dx, w, H, n, hpb, (n + hpb - 1) / hpb};
-    };
-    a.side[0] = side(d_q, q, qs, dq, qw, Hq);
-    a.side[1] = side(d_k, k, ks, dk, kw, Hkv);
     int nq, nk;
     grad_grid(a.n_tok, Hq, Hkv, D, sms, &nq, &nk);
+    auto side = [&](const void *dy, const uint16_t *x, int64_t xs, void *dx, const float *w,
+                    int H, int blocks) {
+        const int n = (H + GRAD_ROWS - 1) / GRAD_ROWS;
+        const int hpb = batches_per_item(a.n_tok, n, (int64_t)blocks * THREADS / lanes, 0.5);
+        return Side{dy, x, xs, dx, w, H, n, hpb, (n + hpb - 1) / hpb};
+    };
+    a.side[0] = side(d_q, q, qs, dq, qw, Hq, nq);
+    a.side[1] = side(d_k, k, ks, dk, kw, Hkv, nk);
     a.n_blocks_q = nq;
     a.part = dqw || dkw ? reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kWsHeader)
                         : nullptr;
