@@ -92,26 +92,18 @@ bool tensor_map_2d_bf16(CUtensorMap *out, const void *base, uint64_t rows, uint3
     return true;
 }
 
-// Two caches [B, rows, cols] bf16 in boxes of 64 columns (128-byte swizzle) x box_rows rows;
-// rows from `rows` on read as zeros.  One descriptor for both: the fourth coordinate, *k_at
-// or *v_at, is the cache.  Encoded on every call (a user's caches come and go), and
-// encoding is a tenth of a short call's host time.
-bool tensor_map_caches_bf16(CUtensorMap *out, const void *k, const void *v, uint64_t B,
-                            uint64_t rows, uint32_t cols, uint32_t box_rows, int *k_at,
-                            int *v_at) {
+// A cache [B, rows, cols] bf16 in boxes of 64 columns (128-byte swizzle) x box_rows rows;
+// rows from `rows` on read as zeros.  Encoded on every call: a user's caches come and go.
+bool tensor_map_cache_bf16(CUtensorMap *out, const void *base, uint64_t B, uint64_t rows,
+                           uint32_t cols, uint32_t box_rows) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    const uintptr_t pk = reinterpret_cast<uintptr_t>(k), pv = reinterpret_cast<uintptr_t>(v);
-    const uintptr_t lo = pk < pv ? pk : pv, hi = pk < pv ? pv : pk;
-    *k_at = pk > pv;
-    *v_at = pv > pk;
-    const cuuint64_t row = (cuuint64_t)cols * 2;
-    const cuuint64_t dims[4] = {cols, rows, B, lo == hi ? 1u : 2u};
-    const cuuint64_t strides[3] = {row, row * rows, lo == hi ? row * rows * B : hi - lo};
-    const cuuint32_t box[4] = {64, box_rows, 1, 1};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    return fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, reinterpret_cast<void *>(lo), dims,
-              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    const cuuint64_t dims[3] = {cols, rows, B};
+    const cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)cols * 2 * rows};
+    const cuuint32_t box[3] = {64, box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
+              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

@@ -32,9 +32,8 @@ cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, dim3 block, size
 }
 bool tensor_map_2d_bf16(CUtensorMap_st *out, const void *base, uint64_t rows, uint32_t cols,
                         uint32_t box_rows);
-bool tensor_map_caches_bf16(CUtensorMap_st *out, const void *k, const void *v, uint64_t B,
-                            uint64_t rows, uint32_t cols, uint32_t box_rows, int *k_at,
-                            int *v_at);
+bool tensor_map_cache_bf16(CUtensorMap_st *out, const void *base, uint64_t B, uint64_t rows,
+                           uint32_t cols, uint32_t box_rows);
 
 cudaError_t launch_pool(const uint16_t *k_idx, int B, int64_t T, int Di, int64_t j0,
                         int64_t j1, uint16_t *kp, cudaStream_t s, int num_sms);

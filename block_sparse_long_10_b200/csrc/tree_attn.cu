@@ -62,7 +62,6 @@ struct Args {
     Lens lens;
     const int32_t *parent;  // [B, N]
     int B, N, Hq, Hkv, G, lg;  // lg: log2 G
-    int k_at, v_at;            // dense: the caches' coordinates in the tensor map
     float scale_log2;
     // prefix parts: part x holds O[x * D ..] and (max, sum)[x * 2 ..]
     float *part, *ml;
@@ -430,7 +429,8 @@ QSA_DEVICE void visible(const Args &a, const Seg &sg, int i, int pl, uint32_t (&
 
 template <int D, int NT>
 __global__ void __launch_bounds__(THREADS, 1)
-    tree_dense_kernel(const __grid_constant__ CUtensorMap tm, const Args a) {
+    tree_dense_kernel(const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const Args a) {
     using C = Cfg<D, NT>;
     constexpr int SL = C::SLOTS;
     extern __shared__ uint8_t smem_raw[];
@@ -476,10 +476,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == SOFT / 32) {
         // ------------------------------------------------------ producer --
         if (lane == 0) {
-            sm100::prefetch_tensormap(&tm);
+            sm100::prefetch_tensormap(&tm_k);
+            sm100::prefetch_tensormap(&tm_v);
             uint32_t it = 0, drafts = 0;
             bool dead = false;
-            auto put = [&](int cache, int64_t tile, bool cleaned) {
+            auto put = [&](const CUtensorMap *cache, int64_t tile, bool cleaned) {
                 const uint32_t slot = it % SL;
                 if (dead || !wait(&empty[slot], (it / SL) + 1)) {
                     dead = true;
@@ -494,16 +495,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                 sm100::mbar_arrive_expect_tx(bar, C::TILE);
 #pragma unroll
                 for (int at = 0; at < D / 64; ++at)
-                    sm100::tma_load_4d(ring + slot * C::TILE + at * ATOM, &tm, sg.g * D + at * 64,
-                                       (int32_t)(tile * KT), (int32_t)sg.b, cache, bar);
+                    sm100::tma_load_3d(ring + slot * C::TILE + at * ATOM, cache, sg.g * D + at * 64,
+                                       (int32_t)(tile * KT), (int32_t)sg.b, bar);
                 ++it;
             };
             while (walk.next(a, sg)) {
-                put(a.k_at, sg.t0, false);
+                put(&tm_k, sg.t0, false);
                 for (int j = 0; j < sg.n; ++j) {
-                    if (NT == 1 && j + 1 < sg.n) put(a.k_at, sg.t0 + j + 1, false);
-                    put(a.v_at, sg.t0 + j, has_drafts(sg, j));
-                    if (NT == 2 && j + 1 < sg.n) put(a.k_at, sg.t0 + j + 1, false);
+                    if (NT == 1 && j + 1 < sg.n) put(&tm_k, sg.t0 + j + 1, false);
+                    put(&tm_v, sg.t0 + j, has_drafts(sg, j));
+                    if (NT == 2 && j + 1 < sg.n) put(&tm_k, sg.t0 + j + 1, false);
                 }
             }
             // no copy may land after the CTA has gone
@@ -724,11 +725,11 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // ------------------------------------------------------------------ merge --
-// A query head in a group of 8 lanes, E = D / 8 dims a lane: running (max, sum, O).
+// A (row, head) in a group of 8 lanes, E = D / 8 dims a lane: running (max, sum, O).
 template <int D>
 struct Row {
     static constexpr int E = D / 8;
-    float q[E], o[E];
+    float o[E];
     float m, l;
 
     struct Raw {
@@ -749,10 +750,7 @@ struct Row {
             }
         }
     };
-    QSA_DEVICE void start(const uint16_t *qrow, int li) {
-        Raw x;
-        x.load(qrow + li * E);
-        x.get(q);
+    QSA_DEVICE void start() {
         m = -INFINITY;
         l = 0.f;
 #pragma unroll
@@ -768,22 +766,20 @@ struct Row {
         for (int e = 0; e < E; ++e) o[e] = o[e] * fa + o2[e] * fb;
         m = mn;
     }
-    // a key's score (all lanes call)
-    QSA_DEVICE float score(const Raw &k, float scale_log2) const {
-        float f[E];
-        float x = 0.f;
-        k.get(f);
+    // of a token that is in m and l already, the values that are not finite (all lanes call)
+    QSA_DEVICE void patch(const Raw &q, const Raw &k, const Raw &v, float scale_log2) {
+        float f[E], x = 0.f;
+        {
+            float g[E];
+            q.get(g);
+            k.get(f);
 #pragma unroll
-        for (int e = 0; e < E; ++e) x += q[e] * f[e];
+            for (int e = 0; e < E; ++e) x += g[e] * f[e];
+        }
         x += __shfl_xor_sync(0xffffffffu, x, 1);
         x += __shfl_xor_sync(0xffffffffu, x, 2);
         x += __shfl_xor_sync(0xffffffffu, x, 4);
-        return x * scale_log2;
-    }
-    // of a token that is in m and l already, the values that are not finite
-    QSA_DEVICE void patch(const Raw &k, const Raw &v, float scale_log2) {
-        const float p = fast_exp2(score(k, scale_log2) - (m == -INFINITY ? 0.f : m));
-        float f[E];
+        const float p = fast_exp2(x * scale_log2 - (m == -INFINITY ? 0.f : m));
         v.get(f);
 #pragma unroll
         for (int e = 0; e < E; ++e)
@@ -824,9 +820,7 @@ __global__ void __launch_bounds__(256, 3) tree_merge_kernel(const Args a) {
         return;
     }
     Row<D> r;
-    r.start(a.q + (row * a.Hq + h) * D, li);
-    const int64_t tok = (int64_t)a.Hkv * D;
-    const int64_t base = (b * a.lens.L_max + sq.P) * tok + (h >> a.lg) * D + li * E;
+    r.start();
     griddep_wait();  // the prefix kernel's parts
     int64_t x0 = 0;
     int parts = 0;
@@ -894,15 +888,19 @@ __global__ void __launch_bounds__(256, 3) tree_merge_kernel(const Args a) {
         r.join_groups();
     }
     // what was cleared in the chain's values, all groups the same token
-    if (!SPARSE && patch)
+    if (!SPARSE && patch) {
+        typename Row<D>::Raw q, k, v;
+        q.load(a.q + (row * a.Hq + h) * D + li * E);
+        const int64_t tok = (int64_t)a.Hkv * D;
+        const int64_t base = (b * a.lens.L_max + sq.P) * tok + (h >> a.lg) * D + li * E;
         for (int j = i; j >= 0;) {
-            typename Row<D>::Raw k, v;
             k.load(a.k + base + j * tok);
             v.load(a.v + base + j * tok);
-            r.patch(k, v, a.scale_log2);
+            r.patch(q, k, v, a.scale_log2);
             const int p = a.parent[b * a.N + j];
             j = (uint32_t)(p + 1) > (uint32_t)j ? -1 : p;
         }
+    }
     if (lane < 8) {
         const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
         uint16_t *orow = a.o + (row * a.Hq + h) * D + li * E;
@@ -945,11 +943,12 @@ Workspace sparse_ws(int B, int N, int Hq, int D) {
 }
 
 template <int D, int NT>
-cudaError_t run_dense(const CUtensorMap &tm, const Args &a, int ctas, cudaStream_t s) {
+cudaError_t run_dense(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, int ctas,
+                      cudaStream_t s) {
     auto kern = tree_dense_kernel<D, NT>;
     const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), Cfg<D, NT>::BYTES);
     if (e != cudaSuccess) return e;
-    kern<<<ctas, THREADS, Cfg<D, NT>::BYTES, s>>>(tm, a);
+    kern<<<ctas, THREADS, Cfg<D, NT>::BYTES, s>>>(tk, tv, a);
     return cudaGetLastError();
 }
 
@@ -1004,16 +1003,17 @@ cudaError_t launch_tree_decode(const uint16_t *q, const uint16_t *k, const uint1
     } else {
         a.units = tree::unit_count(N, a.G);
         a.rows = tree::unit_rows(N, a.G);
-        CUtensorMap tm;
-        if (!tensor_map_caches_bf16(&tm, k, v, B, L_max, Hkv * D, tree::KT, &a.k_at, &a.v_at))
+        CUtensorMap tk, tv;
+        if (!tensor_map_cache_bf16(&tk, k, B, L_max, Hkv * D, tree::KT) ||
+            !tensor_map_cache_bf16(&tv, v, B, L_max, Hkv * D, tree::KT))
             return cudaErrorInvalidValue;
         const bool two = tree::unit_tiles(N, a.G) == 2;
         if (D == 64)
-            e = two ? tree::run_dense<64, 2>(tm, a, sms, s)
-                    : tree::run_dense<64, 1>(tm, a, sms, s);
+            e = two ? tree::run_dense<64, 2>(tk, tv, a, sms, s)
+                    : tree::run_dense<64, 1>(tk, tv, a, sms, s);
         else
-            e = two ? tree::run_dense<128, 2>(tm, a, sms, s)
-                    : tree::run_dense<128, 1>(tm, a, sms, s);
+            e = two ? tree::run_dense<128, 2>(tk, tv, a, sms, s)
+                    : tree::run_dense<128, 1>(tk, tv, a, sms, s);
     }
     if (e != cudaSuccess) return e;
     if (sel) return D == 64 ? tree::run_merge<64, true>(a, s) : tree::run_merge<128, true>(a, s);
