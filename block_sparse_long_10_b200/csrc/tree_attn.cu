@@ -767,7 +767,7 @@ struct Row {
         m = mn;
     }
     // of a token that is in m and l already, the values that are not finite (all lanes call)
-    QSA_DEVICE void patch(const Raw &q, const Raw &k, const Raw &v, float scale_log2) {
+    QSA_DEVICE void patch(const Raw &q, const Raw &k, const Raw &v, bool on, float scale_log2) {
         float f[E], x = 0.f;
         {
             float g[E];
@@ -783,7 +783,7 @@ struct Row {
         v.get(f);
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            if (!(fabsf(f[e]) < INFINITY)) o[e] += p * f[e];
+            if (on && !(fabsf(f[e]) < INFINITY)) o[e] += p * f[e];
     }
     // the warp's four groups' parts become one, in every lane
     QSA_DEVICE void join_groups() {
@@ -799,33 +799,33 @@ struct Row {
     }
 };
 
-// W warps per (row, head): their 4 W groups of 8 lanes share out the parts and (sparse, before
-// the prefix kernel has ended) the chain's tokens, the next ones' loads under the current
-// ones' arithmetic.  W = 1 takes the heads of one KV head into a
-// block, whose loads of the chain meet in L1.
+// The parts of a (row, head) are shared out over the 4 W groups of W warps, or (W = 0) are all
+// one group's, the next one's loads under the current one's arithmetic.
 template <int D, bool SPARSE, int W>
 __global__ void __launch_bounds__(256, 3) tree_merge_kernel(const Args a) {
-    constexpr int E = Row<D>::E;
-    __shared__ float s_o[W > 1 ? W : 1][W > 1 ? D : 1], s_m[W], s_l[W];
-    const int64_t row = blockIdx.x;
-    const int64_t b = row / a.N;
-    const int i = (int)(row - b * a.N);
+    constexpr int E = Row<D>::E, STEP = W == 0 ? 1 : 4 * W;
+    __shared__ float s_o[W > 1 ? W : 1][W > 1 ? D : 1], s_m[W > 1 ? W : 1], s_l[W > 1 ? W : 1];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, li = lane & 7;
-    const int h = W > 1 ? (int)blockIdx.y : (int)(blockIdx.y * (blockDim.x >> 5)) + warp;
-    const int grp = (W > 1 ? warp * 4 : 0) + (lane >> 3);
-    const Seq sq = a.lens.at(b);
-    if (sq.bad) {
-        if (i == 0 && h == 0 && lane == 0) record_status(a.status, QSA_ERR_DEVICE);
-    } else if (i >= sq.n) {
-        return;
-    }
+    // (row, head) pairs: a block's (W > 1), a warp's, a group's
+    const int64_t pairs = (int64_t)a.B * a.N * a.Hq;
+    const int64_t pair = W > 1    ? blockIdx.x
+                         : W == 1 ? (int64_t)blockIdx.x * 8 + warp
+                                  : (int64_t)blockIdx.x * 32 + warp * 4 + (lane >> 3);
+    const int64_t row = pair / a.Hq, b = row / a.N;
+    const int h = (int)(pair - row * a.Hq), i = (int)(row - b * a.N);
+    const int first = W == 0 ? 0 : (W > 1 ? warp * 4 : 0) + (lane >> 3);
+    Seq sq{0, 0, false};
+    if (pair < pairs) sq = a.lens.at(b);
+    if (sq.bad && i == 0 && h == 0 && li == 0) record_status(a.status, QSA_ERR_DEVICE);
+    const bool live = pair < pairs && (sq.bad || i < sq.n);
+    if (W > 0 && !live) return;  // whole warps and blocks; groups stay for the shuffles
     Row<D> r;
     r.start();
     griddep_wait();  // the prefix kernel's parts
     int64_t x0 = 0;
     int parts = 0;
     bool patch = false;  // values of drafts were not finite
-    if (!sq.bad) {
+    if (live && !sq.bad) {
         // unit and row in it
         const int rr = SPARSE ? h : (i << a.lg) + (h & (a.G - 1)), qt = rr / a.rows;
         const int64_t u = SPARSE ? row : (b * a.Hkv + (h >> a.lg)) * a.units + qt;
@@ -845,8 +845,8 @@ __global__ void __launch_bounds__(256, 3) tree_merge_kernel(const Args a) {
         for (int e = 0; e < E / 4; ++e)
             f[e] = reinterpret_cast<const float4 *>(a.part + x * D + li * E)[e];
     };
-    if (grp < parts) fetch(grp);
-    for (int s = grp; s < parts; s += 4 * W) {
+    if (first < parts) fetch(first);
+    for (int s = first; s < parts; s += STEP) {
         float o2[E];
         const float2 c = ml;
 #pragma unroll
@@ -856,11 +856,11 @@ __global__ void __launch_bounds__(256, 3) tree_merge_kernel(const Args a) {
             o2[4 * e + 2] = f[e].z;
             o2[4 * e + 3] = f[e].w;
         }
-        if (s + 4 * W < parts) fetch(s + 4 * W);
+        if (s + STEP < parts) fetch(s + STEP);
         r.join(c.x, c.y, o2);
     }
     __syncwarp();
-    r.join_groups();
+    if (W > 0) r.join_groups();
     if (W > 1) {
         if (lane < 8) {
 #pragma unroll
@@ -873,10 +873,7 @@ __global__ void __launch_bounds__(256, 3) tree_merge_kernel(const Args a) {
         __syncthreads();
         if (warp != 0) return;
         // group g of warp 0 takes the sums of warps g, g + 4, ...
-        r.m = -INFINITY;
-        r.l = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) r.o[e] = 0.f;
+        r.start();
 #pragma unroll
         for (int w = 0; w < W; w += 4) {
             float o2[E];
@@ -887,23 +884,26 @@ __global__ void __launch_bounds__(256, 3) tree_merge_kernel(const Args a) {
         }
         r.join_groups();
     }
-    // what was cleared in the chain's values, all groups the same token
-    if (!SPARSE && patch) {
+    // what was cleared in the chain's values (W > 0: all groups the same token)
+    if (!SPARSE && __any_sync(0xffffffffu, patch)) {
         typename Row<D>::Raw q, k, v;
-        q.load(a.q + (row * a.Hq + h) * D + li * E);
         const int64_t tok = (int64_t)a.Hkv * D;
         const int64_t base = (b * a.lens.L_max + sq.P) * tok + (h >> a.lg) * D + li * E;
-        for (int j = i; j >= 0;) {
-            k.load(a.k + base + j * tok);
-            v.load(a.v + base + j * tok);
-            r.patch(q, k, v, a.scale_log2);
-            const int p = a.parent[b * a.N + j];
-            j = (uint32_t)(p + 1) > (uint32_t)j ? -1 : p;
+        q.load(a.q + (patch ? pair : 0) * D + li * E);
+        for (int j = patch ? i : -1; __any_sync(0xffffffffu, j >= 0);) {
+            const int64_t at = j >= 0 ? base + j * tok : 0;
+            k.load(a.k + at);
+            v.load(a.v + at);
+            r.patch(q, k, v, j >= 0, a.scale_log2);
+            if (j >= 0) {
+                const int p = a.parent[b * a.N + j];
+                j = (uint32_t)(p + 1) > (uint32_t)j ? -1 : p;
+            }
         }
     }
-    if (lane < 8) {
+    if (live && (W == 0 || lane < 8)) {
         const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
-        uint16_t *orow = a.o + (row * a.Hq + h) * D + li * E;
+        uint16_t *orow = a.o + pair * D + li * E;
 #pragma unroll
         for (int e = 0; e < E; e += 8)
             *reinterpret_cast<uint4 *>(orow + e) =
@@ -912,7 +912,7 @@ __global__ void __launch_bounds__(256, 3) tree_merge_kernel(const Args a) {
                            pack_bf16x2(r.o[e + 4] * inv, r.o[e + 5] * inv),
                            pack_bf16x2(r.o[e + 6] * inv, r.o[e + 7] * inv));
         if (a.lse && li == 0)
-            a.lse[row * a.Hq + h] = r.l == 0.f ? -INFINITY : (r.m + __log2f(r.l)) * LN2;
+            a.lse[pair] = r.l == 0.f ? -INFINITY : (r.m + __log2f(r.l)) * LN2;
     }
 }
 
@@ -952,16 +952,20 @@ cudaError_t run_dense(const CUtensorMap &tk, const CUtensorMap &tv, const Args &
     return cudaGetLastError();
 }
 
-// 8 warps a (row, head) pair where all pairs' blocks run at once (3 on each of 148 SMs): few
-// pairs may have many parts each.
+// 8 warps a (row, head) where all of them run at once (3 blocks on each of 148 SMs): few pairs
+// may have many parts each.  A group of 8 lanes from two rounds of 24 warps an SM on, a warp
+// between (whole call, group / warp: 65536 pairs 44.5 / 67 us, 8192 23.2 / 25.6, 4096 76.0 / 74.6).
 template <int D, bool SPARSE>
 cudaError_t run_merge(const Args &a, cudaStream_t s) {
-    const int64_t rows = (int64_t)a.B * a.N;
-    if (rows * a.Hq <= 148 * 3)
-        return launch_dependent(tree_merge_kernel<D, SPARSE, 8>, dim3((unsigned)rows, a.Hq),
+    const int64_t pairs = (int64_t)a.B * a.N * a.Hq;
+    if (pairs <= 148 * 3)
+        return launch_dependent(tree_merge_kernel<D, SPARSE, 8>, dim3((unsigned)pairs), dim3(256), 0,
+                                s, a);
+    if (pairs <= 148 * 48)
+        return launch_dependent(tree_merge_kernel<D, SPARSE, 1>, dim3((unsigned)((pairs + 7) / 8)),
                                 dim3(256), 0, s, a);
-    return launch_dependent(tree_merge_kernel<D, SPARSE, 1>, dim3((unsigned)rows, a.Hkv),
-                            dim3(a.G * 32), 0, s, a);
+    return launch_dependent(tree_merge_kernel<D, SPARSE, 0>, dim3((unsigned)((pairs + 31) / 32)),
+                            dim3(256), 0, s, a);
 }
 
 }  // namespace tree
