@@ -201,6 +201,70 @@ def test_norm_rope_slot_out_of_range_is_recorded_and_not_written():
     assert qsa.qsa_check_device_status(ws) == 0
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,rot", [(16, 2, 128, 128), (5, 3, 64, 24), (4, 1, 256, 256)])
+def test_rows_do_not_depend_on_their_batch(Hq, Hkv, D, rot):
+    """A token's rows have the same bits in a batch of thousands (many rounds of the GPU, several
+    rows at a time) and in one of dozens."""
+    g = _gen(D + rot)
+    B, T, cut = 2, 9001, 60
+    packed = _randn(g, B, T, (Hq + 2 * Hkv) * D)
+    part = lambda x: (x[..., :Hq * D].unflatten(-1, (Hq, D)),
+                      x[..., Hq * D:(Hq + Hkv) * D].unflatten(-1, (Hkv, D)),
+                      x[..., (Hq + Hkv) * D:].unflatten(-1, (Hkv, D)))
+    f, m = _freq(rot, "by-parts")
+    qw, kw = _weights(g, D, (True, True))
+    pos = torch.randint(0, 1 << 20, (B, T), generator=g, device=DEV)
+    d = {t: (_randn(g, B, T, Hq, D, dtype=t), _randn(g, B, T, Hkv, D, dtype=t)) for t in (BF, F32)}
+
+    def run(lo, hi):
+        p = pos[:, lo:hi].contiguous()
+        q, k, v = part(packed[:, lo:hi].contiguous())
+        kwargs = dict(q_weight=qw, k_weight=kw, pos=p, mscale=m)
+        out = [torch.empty(B, hi - lo, h, D, dtype=BF, device=DEV) for h in (Hq, Hkv, Hkv)]
+        qsa.qsa_qk_norm_rope(q, k, out[0], out[1], f, v=v, v_out=out[2], **kwargs)
+        for t, (dq, dk) in d.items():
+            a, b = dq[:, lo:hi].contiguous(), dk[:, lo:hi].contiguous()
+            out += [torch.empty_like(a), torch.empty_like(b), torch.empty_like(a)]
+            qsa.qsa_qk_norm_rope_backward(a, b, q, k, out[-3], out[-2], f, **kwargs)
+            qsa.qsa_rope(a, out[-1], f, pos=p, mscale=m, transpose=True)
+        return out
+
+    whole = run(0, T)
+    for lo in (0, 4000, T - cut):
+        for a, b in zip(whole, run(lo, lo + cut)):
+            assert torch.equal(a[:, lo:lo + cut], b)
+
+
+def test_refusals():
+    g = _gen(2)
+    q, k = _randn(g, 2, 3, 4, 64), _randn(g, 2, 3, 2, 64)
+    f, _ = _freq(64)
+    w, pos = torch.ones(64, device=DEV), torch.zeros(2, 3, dtype=torch.int64, device=DEV)
+    e = torch.empty_like
+    for error, call in (
+            (TypeError, lambda: qsa.qsa_rope(q, e(q).float(), f)),
+            (ValueError, lambda: qsa.qsa_rope(q, e(q)[:, :2], f)),
+            (TypeError, lambda: qsa.qsa_rope(q, e(q), f.float())),
+            (ValueError, lambda: qsa.qsa_rope(q, e(q), f.cpu())),
+            (ValueError, lambda: qsa.qsa_rope(q, e(q), f, layout="pairs")),
+            (ValueError, lambda: qsa.qsa_rope(q.transpose(1, 2), e(q).transpose(1, 2), f)),
+            (ValueError, lambda: qsa.qsa_rope(q, e(q), f, pos=pos[:1])),
+            (qsa.QSAError, lambda: qsa.qsa_rope(q, e(q), f, mscale=float("inf"))),
+            (qsa.QSAError, lambda: qsa.qsa_rope(q, e(q), f[:3])),
+            (ValueError, lambda: qsa.qsa_qk_norm_rope(q, k, e(q), e(k), f, v=k)),
+            (ValueError, lambda: qsa.qsa_qk_norm_rope(q, k, e(q), e(k)[:, :2], f)),
+            (TypeError, lambda: qsa.qsa_qk_norm_rope(q, k, e(q), e(k), f, q_weight=w.double())),
+            (ValueError, lambda: qsa.qsa_qk_norm_rope(q, k, e(q), e(k), f, q_weight=w[:32])),
+            (ValueError, lambda: qsa.qsa_qk_norm_rope(q, k, e(q), e(k), f, ws=qsa.workspace(128))),
+            (TypeError, lambda: qsa.qsa_qk_norm_rope(q, k, e(q), e(k), f, slot=pos.int())),
+            (qsa.QSAError, lambda: qsa.qsa_qk_norm_rope(q, k, e(q), e(k), f, eps=-1.0)),
+            (TypeError, lambda: qsa.qsa_qk_norm_rope_backward(q, k.float(), q, k, e(q), e(k), f)),
+            (qsa.QSAError, lambda: qsa.qsa_qk_norm_rope_backward(
+                q, k, q, k, e(q), e(k), f, q_weight=w, dq_weight=e(w)))):  # no workspace
+        with pytest.raises(error):
+            call()
+
+
 def test_norm_of_zero_and_huge_rows():
     """A row of zeros stays zero (eps > 0); rows of 2^60 keep their norm: their squares
     (2^120) and sums stay below fp32's range."""

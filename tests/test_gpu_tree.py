@@ -208,6 +208,71 @@ def test_other_branches_may_hold_anything(sparse):
         assert not bool(torch.isfinite(o[0, 3].float()).all())
 
 
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,top", [(1, 9, 8, 2, 64, 250), (2, 40, 16, 2, 128, 380),
+                                              (9, 64, 16, 2, 128, 120), (1, 256, 8, 1, 64, 77)])
+def test_infinite_values_reach_their_descendants_only(B, N, Hq, Hkv, D, top):
+    """One infinite value of a draft: that dim of its descendants' heads becomes infinite (their
+    weight on the draft is not zero), every other bit stays."""
+    prefix, drafts = [top - 5 * b for b in range(B)], [N - b % 3 for b in range(B)]
+    x = _make(B, N, Hq, Hkv, D, prefix, drafts, seed=41)
+    good = _run(x)
+    for j, g, d, bad in ((N // 3, Hkv - 1, D - 1, float("inf")), (0, 0, 3, float("-inf"))):
+        y = dict(x, v=x["v"].clone())
+        for b in range(B):
+            y["v"][b, prefix[b] + j, g, d] = bad
+        o, lse, ws = _run(y)
+        assert qsa.qsa_check_device_status(ws) == 0
+        want = good[0].clone()
+        G = Hq // Hkv
+        for b in range(B):
+            for i in range(drafts[b]):
+                if prefix[b] + j in tree.tokens(prefix[b], i, x["parent"][b].tolist()):
+                    want[b, i, g * G:(g + 1) * G, d] = bad
+        assert torch.equal(o, want) and torch.equal(lse, good[1])
+
+
+def test_nan_in_a_row_of_the_prefix_reaches_every_row():
+    """A key that is not a number is in every row's sum."""
+    x = _make(1, 6, 8, 1, 128, [700], [6], seed=43)
+    for at in (0, 130, 699):
+        y = dict(x, k=x["k"].clone())
+        y["k"][0, at, 0, 5] = float("nan")
+        o, lse, _ = _run(y)
+        assert bool(o.isnan().all()) and bool(lse.isnan().all())
+    y = dict(x, k=x["k"].clone())  # an infinite score: inf - inf
+    y["k"][0, 200, 0] = float("inf")
+    y["q"] = x["q"].abs()
+    o, lse, _ = _run(y)
+    assert bool(o.isnan().all())
+
+
+def test_refusals():
+    x = _make(2, 4, 8, 2, 64, [30, 40], [4, 4], seed=44)
+    sel = _sel([30, 40], 4, 16, 1)
+    ws = qsa.workspace(qsa.qsa_sparse_tree_decode_workspace_size(2, 4, 8, 64, 4, 64), DEV)
+    ws = qsa.workspace(max(ws.numel(), qsa.qsa_dense_tree_decode_workspace_size(2, 4, 8, 2, 64)),
+                       DEV)
+    base = dict(q=x["q"], k_cache=x["k"], v_cache=x["v"], seqlens=x["seqlens"],
+                parent=x["parent"], o=torch.empty_like(x["q"]), ws=ws)
+    bad = [(TypeError, dict(q=x["q"].float())), (TypeError, dict(seqlens=x["seqlens"].long())),
+           (TypeError, dict(k_cache=None)), (ValueError, dict(v_cache=x["v"][:, :-1])),
+           (ValueError, dict(parent=x["parent"][:, :3])), (ValueError, dict(o=base["o"][:1])),
+           (ValueError, dict(parent=x["parent"].T.contiguous().T)), (ValueError, dict(q=x["q"][0])),
+           (ValueError, dict(seqlens=x["seqlens"].cpu())), (qsa.QSAError, dict(ws=None)),
+           (qsa.QSAError, dict(ws=ws[:256])), (qsa.QSAError, dict(scale=float("nan"))),
+           (ValueError, dict(n_draft=x["n_draft"][:1])), (TypeError, dict(lse=base["o"]))]
+    for call, more, extra in (
+            (qsa.qsa_dense_tree_decode, {}, []),
+            (qsa.qsa_sparse_tree_decode, dict(sel=sel, budget=64),
+             [(ValueError, dict(sel=sel[:, :, :15])), (TypeError, dict(sel=sel.long())),
+              (ValueError, dict(sel=sel.transpose(1, 2).contiguous().transpose(1, 2))),
+              (ValueError, dict(budget=60)), (qsa.QSAError, dict(budget=64, r=8, sel=sel[:, :, :8]))])):
+        call(**{**base, **more})
+        for error, kw in bad + extra:
+            with pytest.raises(error):
+                call(**{**base, **more, **kw})
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.1, 1.0])
 def test_scales(scale):
     """Any finite scale; at 1.0 logits reach beyond 100 and the softmax is nearly one-hot
@@ -350,6 +415,36 @@ def test_repeats_and_replays_to_the_same_bits(sparse):
     if sparse:
         sel = sel.clone()
     _check(x, o, lse, [638, 4], [2, 8], sel)
+
+
+def test_on_a_given_stream_and_on_the_current_one():
+    prefix, drafts = [900, 20], [5, 3]
+    x = _make(2, 5, 8, 2, 64, prefix, drafts, seed=51)
+    sel = _sel(prefix, 5, 64, 52)
+    f, _ = qsa.qsa_rope_frequencies(1e4, 64, device=DEV)
+    good = _run(x), _run(x, sel, 256)
+    turned = torch.empty_like(x["q"])
+    qsa.qsa_rope(x["q"], turned, f)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for given in (True, False):
+        o, l = [torch.empty_like(x["q"]) for _ in range(3)], torch.empty(2, 5, 8, device=DEV)
+        for t in o:
+            t.fill_(7.0)
+        side.wait_stream(torch.cuda.current_stream())
+        torch.cuda._sleep(20000000)  # the current stream is busy
+        kw = dict(stream=side) if given else {}
+        with torch.cuda.stream(torch.cuda.current_stream() if given else side):
+            qsa.qsa_dense_tree_decode(x["q"], x["k"], x["v"], x["seqlens"], x["parent"], o[0],
+                                      good[0][2], n_draft=x["n_draft"], lse=l, **kw)
+            qsa.qsa_sparse_tree_decode(x["q"], x["k"], x["v"], x["seqlens"], sel, x["parent"],
+                                       o[1], good[1][2], n_draft=x["n_draft"], budget=256, **kw)
+            qsa.qsa_rope(x["q"], o[2], f, **kw)
+        side.synchronize()
+        assert not torch.cuda.current_stream().query()  # nothing waited for it
+        assert torch.equal(o[0], good[0][0]) and torch.equal(o[1], good[1][0])
+        assert torch.equal(o[2], turned)
+        torch.cuda.synchronize()
 
 
 def test_norm_rotate_select_attend_together():
