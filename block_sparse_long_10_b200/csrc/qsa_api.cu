@@ -588,7 +588,8 @@ qsa_status_t qsa_qk_norm_rope_backward(
     if ((dq_weight && !q_weight) || (dk_weight && !k_weight)) return QSA_ERR_INVALID_ARG;
     if (!supported_head(D) || rot % 8 != 0) return QSA_ERR_UNSUPPORTED_SHAPE;
     if (T == 0 && !dq_weight && !dk_weight) return QSA_OK;
-    if (T > 0 && (!d_q || !d_k || !q || !k || !dq || !dk || (rot > 0 && !freq)))
+    // (the table is read for T == 0 too: the kernel runs, to write zeros)
+    if ((rot > 0 && !freq) || (T > 0 && (!d_q || !d_k || !q || !k || !dq || !dk)))
         return QSA_ERR_INVALID_ARG;
     if ((dq_weight || dk_weight) &&
         (!ws || !aligned16(ws) ||

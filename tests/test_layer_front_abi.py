@@ -75,6 +75,7 @@ def test_norm_rope_backward(lib):
                 dqw=F, dkw=F, ws=F, wsb=n, s=None)
     call = _caller(lib.qsa_qk_norm_rope_backward, names, good)
     assert call(T=0, dqw=None, dkw=None) == OK
+    assert call(T=0, f=None) == INVALID  # the weight gradients are written: a launch
     for kw in (dict(dq=None), dict(dk=None), dict(q=None), dict(k=None), dict(oq=None),
                dict(ok=None), dict(f=None), dict(dt=2), dict(ot=-1), dict(qw=None), dict(kw=None),
                dict(eps=NAN), dict(lay=3), dict(rot=160), dict(qs=2040), dict(ks=260),
