@@ -612,6 +612,11 @@ qsa_status_t qsa_qk_norm_rope_backward(
 
 // ------------------------------------------- trees of drafted tokens --
 
+// Drafts that a call takes: a row index times 32 query heads fits 31 bits.
+static bool tree_rows(int B, int N) {
+    return N <= qsa::TREE_DRAFTS && (int64_t)B * N <= INT32_MAX / 32;
+}
+
 static qsa_status_t check_tree(const void *q, const void *k, const void *v, const void *seqlens,
                                int64_t L_max, const void *parent, int B, int N, int Hq, int Hkv,
                                int D, float scale, const void *o) {
@@ -619,8 +624,7 @@ static qsa_status_t check_tree(const void *q, const void *k, const void *v, cons
         !isfinite(scale))
         return QSA_ERR_INVALID_ARG;
     if (!q || !k || !v || !seqlens || !parent || !o) return QSA_ERR_INVALID_ARG;
-    if (!supported_attn(Hq, Hkv, D) || N > qsa::TREE_DRAFTS ||
-        (int64_t)B * N > INT32_MAX / 32 || L_max > INT32_MAX)
+    if (!supported_attn(Hq, Hkv, D) || !tree_rows(B, N) || L_max > INT32_MAX)
         return QSA_ERR_UNSUPPORTED_SHAPE;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o))
         return QSA_ERR_INVALID_ARG;
@@ -628,7 +632,9 @@ static qsa_status_t check_tree(const void *q, const void *k, const void *v, cons
 }
 
 size_t qsa_dense_tree_decode_workspace_size(int B, int N, int Hq, int Hkv, int D) {
-    if (B < 1 || N < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1) return SIZE_MAX;
+    if (B < 1 || N < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !tree_rows(B, N) ||
+        !supported_attn(Hq, Hkv, D))
+        return SIZE_MAX;
     return qsa::tree_dense_ws_bytes(B, N, Hq, Hkv, D);
 }
 
@@ -652,7 +658,8 @@ qsa_status_t qsa_dense_tree_decode(const qsa_bf16_t *q, const qsa_bf16_t *k_cach
 }
 
 size_t qsa_sparse_tree_decode_workspace_size(int B, int N, int Hq, int D, int r, int budget) {
-    if (B < 1 || N < 1 || Hq < 1 || D < 1 || r < 1 || budget < r || budget % r != 0)
+    if (B < 1 || N < 1 || Hq < 1 || r < 1 || budget < r || budget % r != 0 ||
+        !tree_rows(B, N) || Hq > 32 || (D != 64 && D != 128))
         return SIZE_MAX;
     return qsa::tree_sparse_ws_bytes(B, N, Hq, D);
 }

@@ -91,10 +91,13 @@ def test_tree_decode(lib):
     m = lib.qsa_sparse_tree_decode_workspace_size(2, 8, 16, 128, 4, 2048)
     assert 256 < n < SIZE_MAX and 256 < m < SIZE_MAX
     for bad in ((0, 8, 16, 2, 128), (2, 0, 16, 2, 128), (2, 8, 16, 3, 128), (2, 8, 16, 0, 128),
-                (2, 8, 16, 2, 0)):
+                (2, 8, 16, 2, 0), (2, 257, 16, 2, 128), (2 ** 24, 8, 16, 2, 128),
+                (1, 65536, 65536, 1, 128), (2, 8, 16, 2, 96)):
         assert lib.qsa_dense_tree_decode_workspace_size(*bad) == SIZE_MAX, bad
     for bad in ((0, 8, 16, 128, 4, 2048), (2, 8, 16, 128, 0, 2048), (2, 8, 16, 128, 4, 2),
-                (2, 8, 16, 128, 4, 2047)):
+                (2, 8, 16, 128, 4, 2047), (2, 257, 16, 128, 4, 2048),
+                (2 ** 24, 8, 16, 128, 4, 2048), (2, 8, 2 ** 30, 128, 4, 2048),
+                (2, 8, 16, 96, 4, 2048)):
         assert lib.qsa_sparse_tree_decode_workspace_size(*bad) == SIZE_MAX, bad
     dense = "q k v sl L par nd B N Hq Hkv D sc o lse ws wsb s".split()
     sparse = "q k v sl L sel sb sn par nd B N Hq Hkv D r bud sc o lse ws wsb s".split()
