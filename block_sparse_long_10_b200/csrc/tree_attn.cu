@@ -110,7 +110,7 @@ struct Cfg {
     static constexpr int SLOTS = FIT > 8 ? 8 : FIT;
     static constexpr int OFF_BAR = OFF_RING + SLOTS * TILE;
     static constexpr int BYTES = 1024 + OFF_BAR + 512;
-    static_assert((4 * SLOTS + 6) * 8 + 16 <= 512, "barriers");
+    static_assert((4 * SLOTS + 8) * 8 + 16 <= 512, "barriers");
     static_assert(NT == 2 || 2 * 128 * 8 <= TILE, "the streams' sums fit in the query tile");
     // TMEM columns
     static constexpr int O_COL = 256;
@@ -297,7 +297,8 @@ QSA_DEVICE void mask_tile(uint32_t s_tm, const uint32_t (&ok)[4]) {
 
 // Softmax of one row's 128 scores: scores in TMEM at s_tm become bf16 probabilities in its
 // first 64 columns; the row's maximum, sum and (at o_tm, if there is one) O move along.
-// Whole warps.
+// `phalf` learns when the first 64 tokens' are there: their half of O += P V runs under the
+// rest.  Whole warps.
 //
 // The exponential unit does 16 a clock and SM, so 128 x 128 of them take as long as the
 // tile's two matrix products; POLY of every 8 pairs go to the FMA pipe instead.
@@ -306,7 +307,8 @@ QSA_DEVICE void mask_tile(uint32_t s_tm, const uint32_t (&ok)[4]) {
 // probability of the row.
 constexpr int POLY = 3;
 template <int D>
-QSA_DEVICE void soft_tile(uint32_t s_tm, uint32_t o_tm, float sc, bool has_o, float &m, float &l) {
+QSA_DEVICE void soft_tile(uint32_t s_tm, uint32_t o_tm, float sc, bool has_o, float &m, float &l,
+                          uint64_t *phalf) {
     // The scores are read twice, 32 at a time: all 128 in registers would spill.
     uint32_t x[2][32];
     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -364,6 +366,11 @@ QSA_DEVICE void soft_tile(uint32_t s_tm, uint32_t o_tm, float sc, bool has_o, fl
             pk[e / 2] = pack_bf16x2(p0, p1);
         }
         sm100::tmem_st16(s_tm + c / 2, pk);
+        if (c + 32 == KT / 2) {
+            sm100::tmem_wait_st();
+            sm100::tc_fence_before();
+            sm100::mbar_arrive(phalf);
+        }
     }
     float a, b;
     unpair(add2(sum[0], sum[1]), a, b);
@@ -437,7 +444,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR), *empty = full + SL;
     uint64_t *dfull = empty + SL, *clean = dfull + SL;  // drafts' values have come; are clean
-    uint64_t *sfull = clean + SL, *pready = sfull + 2, *odone = pready + 2, *qready = odone + 1;
+    uint64_t *sfull = clean + SL, *phalf = sfull + 2, *pready = phalf + 2,
+             *odone = pready + 2, *qready = odone + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(qready + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -455,6 +463,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         for (int i = 0; i < 2; ++i) {
             sm100::mbar_init(&sfull[i], 1);
+            sm100::mbar_init(&phalf[i], 128);
             sm100::mbar_init(&pready[i], 128);
         }
         sm100::mbar_init(odone, 1);
@@ -545,7 +554,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int t = 0; t < steps; ++t) {
                 const int s = t & 1;
                 const uint32_t idx = ring_v<NT>(base, NT == 2 ? t >> 1 : t, n), slot = idx % SL;
-                wait(&pready[s], done[s]++);
+                wait(&phalf[s], done[s]);
                 if (NT == 1 || s == 0) {
                     wait(&full[slot], idx / SL);
                     if (has_drafts(sg, NT == 2 ? t >> 1 : t)) {
@@ -555,11 +564,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 sm100::tc_fence_after();
                 const uint64_t va = sm100::smem_desc_mnmajor(ring + slot * C::TILE, ATOM);
+                auto weigh = [&](int k) {
+                    sm100::mma_bf16_ta(tmem + C::O_COL + s * D, tmem + s * KT + k * 8,
+                                       va + k * (2048 >> 4), C::IDESC_O, t > 1 || k > 0);
+                };
                 if (leader) {
 #pragma unroll
-                    for (int k = 0; k < KT / 16; ++k)
-                        sm100::mma_bf16_ta(tmem + C::O_COL + s * D, tmem + s * KT + k * 8,
-                                           va + k * (2048 >> 4), C::IDESC_O, t > 1 || k > 0);
+                    for (int k = 0; k < KT / 32; ++k) weigh(k);
+                }
+                wait(&pready[s], done[s]++);
+                sm100::tc_fence_after();
+                if (leader) {
+#pragma unroll
+                    for (int k = KT / 32; k < KT / 16; ++k) weigh(k);
                     if (NT == 1 || s == 1) sm100::mma_commit(&empty[slot]);
                 }
                 if (t + 2 < steps) scores(t + 2);
@@ -658,7 +675,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 sm100::tc_fence_after();
                 if (on) {
                     if (drafts) mask_tile(s_tm, ok);
-                    soft_tile<D>(s_tm, o_tm, sc, t > 1, m, l);
+                    soft_tile<D>(s_tm, o_tm, sc, t > 1, m, l, &phalf[s]);
+                } else {
+                    sm100::mbar_arrive(&phalf[s]);
                 }
                 sm100::tc_fence_before();
                 sm100::mbar_arrive(&pready[s]);
