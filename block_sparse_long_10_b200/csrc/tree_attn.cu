@@ -744,10 +744,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // ------------------------------------------------------------------ merge --
-// A (row, head) in a group of 8 lanes, E = D / 8 dims a lane: running (max, sum, O).
-template <int D>
+// A (row, head) in a group of LANES lanes, E dims a lane: running (max, sum, O).
+template <int D, int LANES>
 struct Row {
-    static constexpr int E = D / 8;
+    static constexpr int E = D / LANES;
     float o[E];
     float m, l;
 
@@ -795,19 +795,18 @@ struct Row {
 #pragma unroll
             for (int e = 0; e < E; ++e) x += g[e] * f[e];
         }
-        x += __shfl_xor_sync(0xffffffffu, x, 1);
-        x += __shfl_xor_sync(0xffffffffu, x, 2);
-        x += __shfl_xor_sync(0xffffffffu, x, 4);
+#pragma unroll
+        for (int i = 1; i < LANES; i <<= 1) x += __shfl_xor_sync(0xffffffffu, x, i);
         const float p = fast_exp2(x * scale_log2 - (m == -INFINITY ? 0.f : m));
         v.get(f);
 #pragma unroll
         for (int e = 0; e < E; ++e)
             if (on && !(fabsf(f[e]) < INFINITY)) o[e] += p * f[e];
     }
-    // the warp's four groups' parts become one, in every lane
+    // the parts of the warp's groups become one, in every lane
     QSA_DEVICE void join_groups() {
 #pragma unroll
-        for (int x = 8; x < 32; x <<= 1) {
+        for (int x = LANES; x < 32; x <<= 1) {
             float o2[E];
             const float m2 = __shfl_xor_sync(0xffffffffu, m, x);
             const float l2 = __shfl_xor_sync(0xffffffffu, l, x);
@@ -818,27 +817,32 @@ struct Row {
     }
 };
 
-// The parts of a (row, head) are shared out over the 4 W groups of W warps, or (W = 0) are all
-// one group's, the next one's loads under the current one's arithmetic.
+// The parts of a (row, head) are shared out over the groups of W warps, or (W = 0) are all
+// one group's; the loads of U of them are issued together.  Groups of D / 8 lanes keep the
+// registers down to 64, four blocks an SM, where a warp has a pair; where a group has one,
+// 8 lanes: there what a warp does once is most of it (32 x 64 drafts behind 100 tokens 26.8 us,
+// with 16 lanes 28.8).
 template <int D, bool SPARSE, int W>
-__global__ void __launch_bounds__(256, 3) tree_merge_kernel(const Args a) {
-    constexpr int E = Row<D>::E, STEP = W == 0 ? 1 : 4 * W;
+__global__ void __launch_bounds__(256, W == 1 ? 4 : 3) tree_merge_kernel(const Args a) {
+    constexpr int LANES = W == 0 ? 8 : D / 8, GROUPS = 32 / LANES;
+    using R = Row<D, LANES>;
+    constexpr int E = R::E, STEP = W == 0 ? 1 : GROUPS * W, U = W == 0 ? 1 : 2;
     __shared__ float s_o[W > 1 ? W : 1][W > 1 ? D : 1], s_m[W > 1 ? W : 1], s_l[W > 1 ? W : 1];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, li = lane & 7;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, li = lane % LANES;
     // (row, head) pairs: a block's (W > 1), a warp's, a group's
     const int64_t pairs = (int64_t)a.B * a.N * a.Hq;
     const int64_t pair = W > 1    ? blockIdx.x
                          : W == 1 ? (int64_t)blockIdx.x * 8 + warp
-                                  : (int64_t)blockIdx.x * 32 + warp * 4 + (lane >> 3);
+                                  : ((int64_t)blockIdx.x * 8 + warp) * GROUPS + lane / LANES;
     const int64_t row = pair / a.Hq, b = row / a.N;
     const int h = (int)(pair - row * a.Hq), i = (int)(row - b * a.N);
-    const int first = W == 0 ? 0 : (W > 1 ? warp * 4 : 0) + (lane >> 3);
+    const int first = W == 0 ? 0 : (W > 1 ? warp * GROUPS : 0) + lane / LANES;
     Seq sq{0, 0, false};
     if (pair < pairs) sq = a.lens.at(b);
     if (sq.bad && i == 0 && h == 0 && li == 0) record_status(a.status, QSA_ERR_DEVICE);
     const bool live = pair < pairs && (sq.bad || i < sq.n);
     if (W > 0 && !live) return;  // whole warps and blocks; groups stay for the shuffles
-    Row<D> r;
+    R r;
     r.start();
     griddep_wait();  // the prefix kernel's parts
     int64_t x0 = 0;
@@ -855,33 +859,36 @@ __global__ void __launch_bounds__(256, 3) tree_merge_kernel(const Args a) {
             for (int k = 0; k <= (int)((sq.P + sq.n - 1) / KT - sq.P / KT); ++k)
                 patch |= info.cleared[k] != 0;
     }
-    float2 ml;
-    float4 f[E / 4];
-    auto fetch = [&](int s) {
-        const int64_t x = x0 + (int64_t)s * a.rows;
-        ml = *reinterpret_cast<const float2 *>(a.ml + x * 2);
+    for (int s = first; s < parts; s += U * STEP) {
+        float2 ml[U];
+        float4 f[U][E / 4];
 #pragma unroll
-        for (int e = 0; e < E / 4; ++e)
-            f[e] = reinterpret_cast<const float4 *>(a.part + x * D + li * E)[e];
-    };
-    if (first < parts) fetch(first);
-    for (int s = first; s < parts; s += STEP) {
-        float o2[E];
-        const float2 c = ml;
+        for (int n = 0; n < U; ++n) {
+            if (s + n * STEP >= parts) continue;
+            const int64_t x = x0 + (int64_t)(s + n * STEP) * a.rows;
+            ml[n] = *reinterpret_cast<const float2 *>(a.ml + x * 2);
 #pragma unroll
-        for (int e = 0; e < E / 4; ++e) {
-            o2[4 * e] = f[e].x;
-            o2[4 * e + 1] = f[e].y;
-            o2[4 * e + 2] = f[e].z;
-            o2[4 * e + 3] = f[e].w;
+            for (int e = 0; e < E / 4; ++e)
+                f[n][e] = reinterpret_cast<const float4 *>(a.part + x * D + li * E)[e];
         }
-        if (s + STEP < parts) fetch(s + STEP);
-        r.join(c.x, c.y, o2);
+#pragma unroll
+        for (int n = 0; n < U; ++n) {
+            if (s + n * STEP >= parts) continue;
+            float o2[E];
+#pragma unroll
+            for (int e = 0; e < E / 4; ++e) {
+                o2[4 * e] = f[n][e].x;
+                o2[4 * e + 1] = f[n][e].y;
+                o2[4 * e + 2] = f[n][e].z;
+                o2[4 * e + 3] = f[n][e].w;
+            }
+            r.join(ml[n].x, ml[n].y, o2);
+        }
     }
     __syncwarp();
     if (W > 0) r.join_groups();
     if (W > 1) {
-        if (lane < 8) {
+        if (lane < LANES) {
 #pragma unroll
             for (int e = 0; e < E; ++e) s_o[warp][li * E + e] = r.o[e];
             if (li == 0) {
@@ -891,12 +898,12 @@ __global__ void __launch_bounds__(256, 3) tree_merge_kernel(const Args a) {
         }
         __syncthreads();
         if (warp != 0) return;
-        // group g of warp 0 takes the sums of warps g, g + 4, ...
+        // group g of warp 0 takes the sums of warps g, g + GROUPS, ...
         r.start();
 #pragma unroll
-        for (int w = 0; w < W; w += 4) {
+        for (int w = 0; w < W; w += GROUPS) {
             float o2[E];
-            const int ww = w + (lane >> 3);
+            const int ww = w + lane / LANES;
 #pragma unroll
             for (int e = 0; e < E; ++e) o2[e] = s_o[ww][li * E + e];
             r.join(s_m[ww], s_l[ww], o2);
@@ -905,7 +912,7 @@ __global__ void __launch_bounds__(256, 3) tree_merge_kernel(const Args a) {
     }
     // what was cleared in the chain's values (W > 0: all groups the same token)
     if (!SPARSE && __any_sync(0xffffffffu, patch)) {
-        typename Row<D>::Raw q, k, v;
+        typename R::Raw q, k, v;
         const int64_t tok = (int64_t)a.Hkv * D;
         const int64_t base = (b * a.lens.L_max + sq.P) * tok + (h >> a.lg) * D + li * E;
         q.load(a.q + (patch ? pair : 0) * D + li * E);
@@ -920,7 +927,7 @@ __global__ void __launch_bounds__(256, 3) tree_merge_kernel(const Args a) {
             }
         }
     }
-    if (live && (W == 0 || lane < 8)) {
+    if (live && (W == 0 || lane < LANES)) {
         const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
         uint16_t *orow = a.o + pair * D + li * E;
 #pragma unroll
