@@ -978,13 +978,16 @@ cudaError_t run_dense(const CUtensorMap &tk, const CUtensorMap &tv, const Args &
     return cudaGetLastError();
 }
 
-// 8 warps a (row, head) where all of them run at once (3 blocks on each of 148 SMs): few pairs
-// may have many parts each.  A group of 8 lanes from two rounds of 24 warps an SM on, a warp
-// between (whole call, group / warp: 65536 pairs 44.5 / 67 us, 8192 23.2 / 25.6, 4096 76.0 / 74.6).
+// 8 warps a (row, head) where all of them run at once (3 blocks on each of 148 SMs), and in two
+// rounds where a unit, as the grid is shared out, has 16 parts or more (whole call, 8 warps / a
+// warp: 448 pairs of 37 parts 24.7 / 29.0 us, 768 of 18 17.2 / 19.7, but 640 of 5 20.6 / 18.6
+// and 1280 of 18 43.2 / 41.9).  A group of 8 lanes from two rounds of 24 warps an SM on, a warp
+// between (group / warp: 65536 pairs 44.5 / 67 us, 8192 30.8 / 33.7, 4096 76.0 / 74.6).
 template <int D, bool SPARSE>
-cudaError_t run_merge(const Args &a, cudaStream_t s) {
+cudaError_t run_merge(const Args &a, int ctas, cudaStream_t s) {
     const int64_t pairs = (int64_t)a.B * a.N * a.Hq;
-    if (pairs <= 148 * 3)
+    const int64_t units = (int64_t)a.B * (SPARSE ? a.N : a.Hkv * a.units);
+    if (pairs <= 148 * (ctas >= 16 * units ? 6 : 3))
         return launch_dependent(tree_merge_kernel<D, SPARSE, 8>, dim3((unsigned)pairs), dim3(256), 0,
                                 s, a);
     if (pairs <= 148 * 48)
@@ -1022,6 +1025,7 @@ cudaError_t launch_tree_decode(const uint16_t *q, const uint16_t *k, const uint1
     a.part = reinterpret_cast<float *>(w + x.part);
     a.ml = reinterpret_cast<float *>(w + x.ml);
     const int sms = num_sms < tree::MAX_CTAS ? num_sms : tree::MAX_CTAS;
+    const int ctas = sel ? tree_sparse_ctas(sms) : sms;
     cudaError_t e;
     if (sel) {
         a.units = 1;
@@ -1029,7 +1033,7 @@ cudaError_t launch_tree_decode(const uint16_t *q, const uint16_t *k, const uint1
         const TreePrefix t{seqlens, n_draft, parent, N, sel, sel_b, sel_n, kb, a.part, a.ml, &a.info->first, &a.info->last,
                            sizeof(tree::UnitInfo) / 4};
         e = launch_tree_sparse_prefix(q, k, v, t, L_max, B, Hq, Hkv, D, scale, ws,
-                                      tree_sparse_ctas(sms), s);
+                                      ctas, s);
     } else {
         a.units = tree::unit_count(N, a.G);
         a.rows = tree::unit_rows(N, a.G);
@@ -1039,15 +1043,17 @@ cudaError_t launch_tree_decode(const uint16_t *q, const uint16_t *k, const uint1
             return cudaErrorInvalidValue;
         const bool two = tree::unit_tiles(N, a.G) == 2;
         if (D == 64)
-            e = two ? tree::run_dense<64, 2>(tk, tv, a, sms, s)
-                    : tree::run_dense<64, 1>(tk, tv, a, sms, s);
+            e = two ? tree::run_dense<64, 2>(tk, tv, a, ctas, s)
+                    : tree::run_dense<64, 1>(tk, tv, a, ctas, s);
         else
-            e = two ? tree::run_dense<128, 2>(tk, tv, a, sms, s)
-                    : tree::run_dense<128, 1>(tk, tv, a, sms, s);
+            e = two ? tree::run_dense<128, 2>(tk, tv, a, ctas, s)
+                    : tree::run_dense<128, 1>(tk, tv, a, ctas, s);
     }
     if (e != cudaSuccess) return e;
-    if (sel) return D == 64 ? tree::run_merge<64, true>(a, s) : tree::run_merge<128, true>(a, s);
-    return D == 64 ? tree::run_merge<64, false>(a, s) : tree::run_merge<128, false>(a, s);
+    if (sel) return D == 64 ? tree::run_merge<64, true>(a, ctas, s)
+                             : tree::run_merge<128, true>(a, ctas, s);
+    return D == 64 ? tree::run_merge<64, false>(a, ctas, s)
+                   : tree::run_merge<128, false>(a, ctas, s);
 }
 
 }  // namespace qsa

@@ -305,6 +305,24 @@ def test_long_runs(B, N, Hq, Hkv, D, top):
             assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
 
 
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,prefix", [
+    (2, 14, 16, 2, 128, [9001, 4]), (4, 12, 16, 2, 64, [3000, 1, 2999, 130]),
+    (1, 128, 8, 1, 128, [20000]), (3, 64, 16, 2, 128, [7000, 6000, 5]), (1, 256, 32, 4, 64, [4100])])
+def test_many_parts_of_a_row(B, N, Hq, Hkv, D, prefix):
+    """Long prefixes, few units: each row's parts come from many SMs, for one to a few
+    thousand (row, head) pairs."""
+    drafts = [N - b for b in range(B)]
+    x = _make(B, N, Hq, Hkv, D, prefix, drafts, seed=71)
+    o, lse, ws = _run(x)
+    assert qsa.qsa_check_device_status(ws) == 0
+    rows = {0, N // 2, N - B, N - 1}
+    _check(x, o, lse, prefix, drafts, rows=rows)
+    sel = _sel(prefix, N, 512, 72)
+    o, lse, ws = _run(x, sel, 2048)
+    assert qsa.qsa_check_device_status(ws) == 0
+    _check(x, o, lse, prefix, drafts, sel, rows=rows)
+
+
 def test_growing_logits_move_the_running_maximum():
     """Keys that grow along the cache: the maximum moves in every tile."""
     prefix, drafts = [1500], [4]
