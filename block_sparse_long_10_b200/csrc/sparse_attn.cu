@@ -37,6 +37,8 @@ constexpr float LN2 = 0.6931471805599453f;
 // an entry, gathered one by one like the others: nothing of another branch is read.  All
 // rows' stages, in one row, are cut into equal runs, one per CTA; each row that a run meets
 // leaves a part.
+// (8 x 16 drafts, 2048 tokens each of 64K: 39 us for 144 MB from HBM and 268 MB gathered through
+// L2, 3.7 and 6.9 TB/s: rows share blocks but each fetches its own.)
 enum Mode { PREFILL = 0, SPLIT = 1, TREE = 2 };
 
 // Prefill: 2-stage ring, 3 CTAs per SM (12 warps: the gather is latency-bound

@@ -94,6 +94,12 @@ struct Args {
 // factor 256) since its last rescale: sums and O stay far inside fp32, and P keeps bf16's
 // relative precision at any size.  P is rounded to bf16 for the matrix product; the sum
 // is taken of the unrounded values, in fp32.
+//
+// What bounds it.  Up to 128 rows a unit: HBM (32 x 8 drafts over 8K to 16K: the CTAs' runs end
+// 48 to 66 us in, 409 MB; a call is 75 us of graph replays).  More: the chain of a stream's step,
+// softmax about 1500 clocks, its own two products 1024, handing over about 400, against 2048
+// of products for both streams (4 x 64 drafts over 64K: runs of 102 to 119 us, 137 GFLOP, the
+// tensor pipe 58 % busy at the 1.6 GHz that the power limit leaves; a call is 136 to 143 us).
 constexpr int ATOM = KT * 128; // bytes of a 64-column half tile in shared memory
 constexpr int SOFT = 256;      // softmax threads
 constexpr int THREADS = SOFT + 96;   // and a producer, an MMA and a cleaning warp
