@@ -825,14 +825,15 @@ struct Row {
 
 // The parts of a (row, head) are shared out over the groups of W warps, or (W = 0) are all
 // one group's; the loads of U of them are issued together.  Groups of D / 8 lanes keep the
-// registers down to 64, four blocks an SM, where a warp has a pair; where a group has one,
-// 8 lanes: there what a warp does once is most of it (32 x 64 drafts behind 100 tokens 26.8 us,
-// with 16 lanes 28.8).
-template <int D, bool SPARSE, int W>
-__global__ void __launch_bounds__(256, W == 1 ? 4 : 3) tree_merge_kernel(const Args a) {
-    constexpr int LANES = W == 0 ? 8 : D / 8, GROUPS = 32 / LANES;
+// registers down to 64, four blocks an SM.  A group of 8 lanes alone (W = 0) takes a part at a
+// time: with a part or two to a pair what a warp does once is most of it (D = 64, 8192 pairs
+// 21.2 us, with two together 22.7).
+template <int D, bool SPARSE, int W, int LANES>
+__global__ void __launch_bounds__(256, W == 1 || (W == 0 && LANES == 16) ? 4 : 3)
+    tree_merge_kernel(const Args a) {
+    constexpr int GROUPS = 32 / LANES;
     using R = Row<D, LANES>;
-    constexpr int E = R::E, STEP = W == 0 ? 1 : GROUPS * W, U = W == 0 ? 1 : 2;
+    constexpr int E = R::E, STEP = W == 0 ? 1 : GROUPS * W, U = W == 0 && LANES == 8 ? 1 : 2;
     __shared__ float s_o[W > 1 ? W : 1][W > 1 ? D : 1], s_m[W > 1 ? W : 1], s_l[W > 1 ? W : 1];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, li = lane % LANES;
     // (row, head) pairs: a block's (W > 1), a warp's, a group's
@@ -987,20 +988,25 @@ cudaError_t run_dense(const CUtensorMap &tk, const CUtensorMap &tv, const Args &
 // 8 warps a (row, head) where all of them run at once (3 blocks on each of 148 SMs), and in two
 // rounds where a unit, as the grid is shared out, has 16 parts or more (whole call, 8 warps / a
 // warp: 448 pairs of 37 parts 24.7 / 29.0 us, 768 of 18 17.2 / 19.7, but 640 of 5 20.6 / 18.6
-// and 1280 of 18 43.2 / 41.9).  A group of 8 lanes from two rounds of 24 warps an SM on, a warp
-// between (group / warp: 65536 pairs 44.5 / 67 us, 8192 30.8 / 33.7, 4096 76.0 / 74.6).
+// and 1280 of 18 43.2 / 41.9).  A group from two rounds of 24 warps an SM on, a warp between
+// (group / warp: 65536 pairs 44.5 / 67 us, 8192 30.8 / 33.7, 4096 76.0 / 74.6).  The group has
+// D / 8 lanes from two parts a unit on, else 8 (16 / 8 lanes: 8192 pairs of 5 parts 33.0 / 35.0
+// us, 32768 of one 28.8 / 26.8).
 template <int D, bool SPARSE>
 cudaError_t run_merge(const Args &a, int ctas, cudaStream_t s) {
     const int64_t pairs = (int64_t)a.B * a.N * a.Hq;
     const int64_t units = (int64_t)a.B * (SPARSE ? a.N : a.Hkv * a.units);
+    auto launch = [&](auto kern, int per) {
+        return launch_dependent(kern, dim3((unsigned)((pairs + per - 1) / per)), dim3(256), 0, s, a);
+    };
+    constexpr int L = D / 8;
     if (pairs <= 148 * (ctas >= 16 * units ? 6 : 3))
-        return launch_dependent(tree_merge_kernel<D, SPARSE, 8>, dim3((unsigned)pairs), dim3(256), 0,
-                                s, a);
-    if (pairs <= 148 * 48)
-        return launch_dependent(tree_merge_kernel<D, SPARSE, 1>, dim3((unsigned)((pairs + 7) / 8)),
-                                dim3(256), 0, s, a);
-    return launch_dependent(tree_merge_kernel<D, SPARSE, 0>, dim3((unsigned)((pairs + 31) / 32)),
-                            dim3(256), 0, s, a);
+        return launch(tree_merge_kernel<D, SPARSE, 8, L>, 1);
+    if (pairs <= 148 * 48) return launch(tree_merge_kernel<D, SPARSE, 1, L>, 8);
+    // (so many pairs of a sparse call have a part or two each)
+    if constexpr (!SPARSE)
+        if (ctas >= 2 * units) return launch(tree_merge_kernel<D, SPARSE, 0, L>, 8 * 32 / L);
+    return launch(tree_merge_kernel<D, SPARSE, 0, 8>, 32);
 }
 
 }  // namespace tree

@@ -465,6 +465,25 @@ def test_on_a_given_stream_and_on_the_current_one():
         torch.cuda.synchronize()
 
 
+def test_two_calls_at_once():
+    """Calls of two streams, each with its own workspace, share the GPU and no result."""
+    cases = []
+    for seed, prefix, drafts in ((81, [3000, 70], [9, 12]), (82, [40, 5000], [12, 2])):
+        x = _make(2, 12, 16, 2, 128, prefix, drafts, seed=seed)
+        sel = _sel(prefix, 12, 128, seed)
+        cases.append((x, sel, _run(x), _run(x, sel, 512)))
+    torch.cuda.synchronize()
+    streams, results = [torch.cuda.Stream() for _ in cases], []
+    for _ in range(10):
+        for stream, (x, sel, dense, sparse) in zip(streams, cases):
+            with torch.cuda.stream(stream):
+                results.append((_run(x, ws=dense[2]), dense))
+                results.append((_run(x, sel, 512, ws=sparse[2]), sparse))
+    torch.cuda.synchronize()
+    for got, good in results:
+        assert torch.equal(got[0], good[0]) and torch.equal(got[1], good[1])
+
+
 def test_norm_rotate_select_attend_together():
     """A verification step as it is used: drafted tokens' projections are normed, rotated at
     prefix + depth and put into the caches at their rows; the indexer's queries are rotated,
