@@ -227,7 +227,7 @@ QSA_DEVICE uint32_t ring_v(uint32_t base, int j, int n) {
 
 QSA_DEVICE void soft_sync() { asm volatile("bar.sync 1, %0;\n" ::"n"(SOFT) : "memory"); }
 
-// A thread's 32-byte sector in one store.
+// A thread's 32-byte sector in one store (the parts start at a multiple of 32 bytes).
 QSA_DEVICE void store_sector(float *p, const uint32_t *r) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(r[0]),
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -959,13 +959,18 @@ int unit_rows(int N, int G) {
 }
 int unit_count(int N, int G) { return (N * G + unit_rows(N, G) - 1) / unit_rows(N, G); }
 
+// Offsets from the workspace's first multiple of 32 bytes: a caller's need only be aligned to
+// 16, and the parts are stored by whole sectors.
 struct Workspace {
     size_t info, part, ml, bytes;
     Workspace(size_t ctas, size_t units, size_t rows, size_t D) {
         info = kWsHeader;
         part = info + (units * sizeof(UnitInfo) + 255) / 256 * 256;
         ml = part + (ctas + units) * rows * D * 4;
-        bytes = ml + (ctas + units) * rows * 8;
+        bytes = ml + (ctas + units) * rows * 8 + 16;
+    }
+    static uint8_t *base(void *ws) {
+        return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(ws) + 31) / 32 * 32);
     }
 };
 Workspace dense_ws(int B, int N, int Hkv, int G, int D) {
@@ -1026,7 +1031,7 @@ cudaError_t launch_tree_decode(const uint16_t *q, const uint16_t *k, const uint1
                                float scale, uint16_t *o, float *lse, void *ws, int num_sms,
                                cudaStream_t s) {
     tree::Args a{};
-    uint8_t *w = static_cast<uint8_t *>(ws);
+    uint8_t *w = tree::Workspace::base(ws);
     a.q = q; a.k = k; a.v = v; a.lens = tree::Lens{seqlens, n_draft, N, L_max};
     a.parent = parent; a.B = B; a.N = N; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv;
     while (1 << a.lg < a.G) ++a.lg;  // 1, 2, 4 or 8 heads to a KV head
