@@ -657,10 +657,18 @@ qsa_status_t qsa_dense_tree_decode(const qsa_bf16_t *q, const qsa_bf16_t *k_cach
                                              o, lse, ws, sms, static_cast<cudaStream_t>(stream)));
 }
 
+// Sums of the rows' stages are 32-bit in the kernel.
+static bool tree_stages(int B, int N, int Hkv, int kb) {
+    return qsa::tree_sparse_stages(B, N, Hkv, kb) <= INT32_MAX;
+}
+
 size_t qsa_sparse_tree_decode_workspace_size(int B, int N, int Hq, int D, int r, int budget) {
     if (B < 1 || N < 1 || Hq < 1 || r < 1 || budget < r || budget % r != 0 ||
         !tree_rows(B, N) || Hq > 32 || (D != 64 && D != 128))
         return SIZE_MAX;
+    // (the fewest key heads have the fewest stages)
+    const int least = Hq <= 8 ? 1 : Hq <= 16 ? 2 : 4;
+    if (!tree_stages(B, N, least, budget / r)) return SIZE_MAX;
     return qsa::tree_sparse_ws_bytes(B, N, Hq, D);
 }
 
@@ -677,7 +685,8 @@ qsa_status_t qsa_sparse_tree_decode(const qsa_bf16_t *q, const qsa_bf16_t *k_cac
                                  scale, o);
     if (st != QSA_OK) return st;
     if (!sel) return QSA_ERR_INVALID_ARG;
-    if (r != 4 || budget / r > 1024) return QSA_ERR_UNSUPPORTED_SHAPE;
+    if (r != 4 || budget / r > 1024 || !tree_stages(B, N, Hkv, budget / r))
+        return QSA_ERR_UNSUPPORTED_SHAPE;
     if (!ws || ws_bytes < qsa::tree_sparse_ws_bytes(B, N, Hq, D) || !aligned16(ws))
         return QSA_ERR_WORKSPACE;
     int sms = 0;

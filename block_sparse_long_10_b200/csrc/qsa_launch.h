@@ -158,6 +158,8 @@ struct TreePrefix {
     int stride;
 };
 int tree_sparse_ctas(int num_sms);
+// Stages of all rows, with what stands for going over to each: at most INT32_MAX.
+int64_t tree_sparse_stages(int B, int N, int Hkv, int kb);
 cudaError_t launch_tree_sparse_prefix(const uint16_t *q, const uint16_t *k, const uint16_t *v,
                                       const TreePrefix &t, int64_t L_max, int B, int Hq, int Hkv,
                                       int D, float scale, void *status, int ctas,

@@ -93,8 +93,8 @@ struct Args {
 };
 
 // A CTA's run of stages over all live rows, nst stages each and START that stand for what a
-// CTA spends on going over to another row (32 bits: the rows number at most 2^31 / 32,
-// refused beyond; their stages would be 2^31 only with 100 GB of queries.)
+// CTA spends on going over to another row.  (32 bits: a call whose rows have more stages
+// together is refused, tree_sparse_stages.)
 struct TreeRun {
     static constexpr int START = 3;
     int pos, hi, b, b0;  // b0: flat index of sequence b's first stage
@@ -547,13 +547,22 @@ cudaError_t launch_split_decode(const uint16_t *q, const uint16_t *k, const uint
 
 int tree_sparse_ctas(int num_sms) { return num_sms * sat::Ring<sat::TREE>::CTAS; }
 
+// Entries of a row: its selection, the tail, the chain.
+static int tree_sparse_entries(int N, int kb) { return kb + 1 + (N + 3) / 4; }
+
+int64_t tree_sparse_stages(int B, int N, int Hkv, int kb) {
+    const int nbs = sparse_attn_blocks_per_stage(Hkv);
+    return (int64_t)B * N *
+           ((tree_sparse_entries(N, kb) + nbs - 1) / nbs + sat::TreeRun::START);
+}
+
 cudaError_t launch_tree_sparse_prefix(const uint16_t *q, const uint16_t *k, const uint16_t *v,
                                       const TreePrefix &t, int64_t L_max, int B, int Hq, int Hkv,
                                       int D, float scale, void *status, int ctas,
                                       cudaStream_t s) {
     sat::Args a{};
     a.q = q; a.k = k; a.v = v; a.seqlens = t.seqlens; a.B = B; a.Tk = L_max; a.Hq = Hq;
-    a.kb = t.kb + 1 + (t.N + 3) / 4; a.scale_log2 = scale * sat::LOG2E; a.tree = t;
+    a.kb = tree_sparse_entries(t.N, t.kb); a.scale_log2 = scale * sat::LOG2E; a.tree = t;
     a.status = status;
     a.total_items = (int64_t)B * t.N;
     return sat::dispatch<sat::TREE>(a, D, Hq / Hkv, Hkv, ctas, s);

@@ -522,7 +522,7 @@ QSA_API qsa_status_t qsa_qk_norm_rope_backward(
  * Rows i >= n of o and lse are left as they were.  Lengths outside 0 <= n <= N,
  * n <= seqlens[b] <= L_max make every row of the sequence empty (o = 0, lse = -inf),
  * a parent out of range ends its chain; both are recorded as QSA_ERR_DEVICE.
- * 1 <= N <= 256; the attention shapes of qsa_dense_gqa_decode.
+ * 1 <= N <= 256, B * N < 2^26; the attention shapes of qsa_dense_gqa_decode.
  */
 QSA_API size_t qsa_dense_tree_decode_workspace_size(int B, int N, int Hq, int Hkv, int D);
 QSA_API qsa_status_t qsa_dense_tree_decode(const qsa_bf16_t *q, const qsa_bf16_t *k_cache,
@@ -541,7 +541,8 @@ QSA_API qsa_status_t qsa_dense_tree_decode(const qsa_bf16_t *q, const qsa_bf16_t
  * the tail).
  *   sel    int32, row (b, i) of budget / r entries at sel + b * sel_batch_stride +
  *          i * sel_row_stride (elements; a row stride of 0 shares one selection)
- * Constraints besides: r = 4, budget / r <= 1024.
+ * Constraints besides: r = 4, budget / r <= 1024, and B * N rows of
+ * ceil((budget / r + 1 + ceil(N / 4)) * Hkv / 16) + 3 stages are at most 2^31 - 1 stages.
  */
 QSA_API size_t qsa_sparse_tree_decode_workspace_size(int B, int N, int Hq, int D, int r,
                                                      int budget);

@@ -139,3 +139,20 @@ def test_binding_refuses_host_tensors_and_types():
                  lambda: qsa.qsa_sparse_tree_decode(x, x, x, z, z[None, None], z[None], x, None)):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,most", [(4, 4, 64, 30393), (1, 1, 64, 116508),
+                                           (16, 2, 128, 59918)])
+def test_sparse_tree_stages_fit_32_bits(lib, Hq, Hkv, D, most):
+    """256 drafts, a budget of 4096: a row has ceil((1024 + 1 + 64) Hkv / 16) + 3 stages (276,
+    72, 140), and all of B * 256 rows at most 2^31 - 1.  (The calls that fit lack a workspace.)"""
+    names = "q k v sl L sel sb sn par nd B N Hq Hkv D r bud sc o lse ws wsb s".split()
+    good = dict(q=F, k=F, v=F, sl=F, L=1000, sel=F, sb=0, sn=0, par=F, nd=None, B=most, N=256,
+                Hq=Hq, Hkv=Hkv, D=D, r=4, bud=4096, sc=0.1, o=F, lse=None, ws=None, wsb=0, s=None)
+    call = _caller(lib.qsa_sparse_tree_decode, names, good)
+    size = lib.qsa_sparse_tree_decode_workspace_size
+    assert call() == WORKSPACE and size(most, 256, Hq, D, 4, 4096) < SIZE_MAX
+    assert call(B=most + 1) == UNSUPPORTED
+    assert call(B=most + 1, bud=2048) == WORKSPACE  # fewer stages a row
+    # the size function, which is not told Hkv, has none where no Hkv fits
+    assert size(230000, 256, Hq, D, 4, 4096) == SIZE_MAX
