@@ -43,15 +43,18 @@ QSA_DEVICE uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// These say "memory": plain loads and stores of the copied bytes (a thread that reads what it
+// copied itself has no barrier in between) stay on their side of them.
 // 16-byte global -> shared copy; src_bytes == 0 writes zeros (no read).
 QSA_DEVICE void cp_async16(uint32_t dst, const void *src, int src_bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst),
-                 "l"(src), "r"(src_bytes));
+                 "l"(src), "r"(src_bytes)
+                 : "memory");
 }
-QSA_DEVICE void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::); }
+QSA_DEVICE void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int N>
 QSA_DEVICE void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;\n" ::"n"(N));
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 
 // ------------------------------------------------------------ ldmatrix --

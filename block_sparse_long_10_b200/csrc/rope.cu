@@ -268,12 +268,14 @@ struct Line {
     uint32_t w[BYTES / 4];
     QSA_DEVICE static void copy(uint32_t dst, const T *src) {
         if (BYTES == 8)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(dst), "l"(src));
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(dst), "l"(src)
+                         : "memory");
         else
 #pragma unroll
             for (int i = 0; i < BYTES / 16; ++i)
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst + i * 16),
-                             "l"(src + i * (16 / (int)sizeof(T))));
+                             "l"(src + i * (16 / (int)sizeof(T)))
+                             : "memory");
     }
     QSA_DEVICE void fetch(const uint8_t *p) {
         if (BYTES == 8) {
