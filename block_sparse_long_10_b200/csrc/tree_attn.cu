@@ -848,10 +848,13 @@ __global__ void __launch_bounds__(256, W == 1 || (W == 0 && LANES == 16) ? 4 : 3
     if (pair < pairs) sq = a.lens.at(b);
     if (sq.bad && i == 0 && h == 0 && li == 0) record_status(a.status, QSA_ERR_DEVICE);
     const bool live = pair < pairs && (sq.bad || i < sq.n);
-    if (W > 0 && !live) return;  // whole warps and blocks; groups stay for the shuffles
     R r;
     r.start();
-    griddep_wait();  // the prefix kernel's parts
+    // The prefix kernel's parts; and without a row to write too: what follows in the stream
+    // starts when this kernel has ended, and may change lengths that the prefix kernel still
+    // reads.
+    griddep_wait();
+    if (W > 0 && !live) return;  // whole warps and blocks; groups stay for the shuffles
     int64_t x0 = 0;
     int parts = 0;
     bool patch = false;  // values of drafts were not finite

@@ -32,3 +32,28 @@ def test_tree_workspaces_at_any_16_byte_boundary(B, N, Hq, Hkv, D, prefix, spars
         assert qsa.qsa_check_device_status(ws) == 0
         assert torch.equal(o, good[0]) and torch.equal(lse, good[1])
         assert bool((buf[offset + n:] == 0xA5).all()) and bool((buf[:offset] == 0).all())
+
+
+@pytest.mark.parametrize("sparse", [False, True])
+@pytest.mark.parametrize("N,Hq,Hkv", [(1, 1, 1), (2, 8, 2), (4, 16, 2)])
+def test_lengths_change_right_behind_steps_without_drafts(N, Hq, Hkv, sparse):
+    """Steps of which no sequence has a draft write nothing; the lengths change in the stream
+    right behind each call, and the next one has its own."""
+    B, D = 300, 64
+    prefix = [17 + (b * 37) % 400 for b in range(B)]
+    x = _make(B, N, Hq, Hkv, D, prefix, [N] * B, seed=13)
+    sel = _sel(prefix, N, 16, 5) if sparse else None
+    good = _run(x, sel, 64)
+    lens = x["seqlens"].clone(), x["n_draft"].clone()
+    none = lens[0] - N, torch.zeros_like(lens[1])
+    ws, results = good[2], []
+    for step in range(12):
+        for name, value in zip(("seqlens", "n_draft"), lens if step % 3 == 2 else none):
+            x[name].copy_(value)
+        results.append(_run(x, sel, 64, ws=ws))
+    assert qsa.qsa_check_device_status(ws) == 0
+    for step, (o, lse, _) in enumerate(results):
+        if step % 3 == 2:
+            assert torch.equal(o, good[0]) and torch.equal(lse, good[1])
+        else:
+            assert bool((o == 7).all()) and bool((lse == 7).all())
