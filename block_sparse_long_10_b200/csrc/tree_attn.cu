@@ -612,6 +612,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                                 lane);
                 sm100::fence_async_shared();
                 const bool any = __any_sync(0xffffffffu, some);
+                __syncwarp();  // a vote orders no memory: all lanes' stores before the arrival
                 if (lane == 0) {
                     a.info[u].cleared[sg.t0 + j - sg.P / KT] = any;
                     sm100::mbar_arrive(&clean[x]);
