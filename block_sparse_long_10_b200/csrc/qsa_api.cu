@@ -560,6 +560,12 @@ qsa_status_t qsa_qk_norm_rope(const qsa_bf16_t *q, int64_t q_stride, const qsa_b
         !aligned16(ws) || !valid_stride(q_stride, Hq, D, 2) ||
         !valid_stride(k_stride, Hkv, D, 2) || (v && !valid_stride(v_stride, Hkv, D, 2)))
         return QSA_ERR_INVALID_ARG;
+    // in place: a row is written where it was read, by those who read it
+    const bool one = (int64_t)B * T == 1;
+    if ((q == q_out && !one && q_stride != (int64_t)Hq * D) ||
+        (k == k_out && (slot || (!one && k_stride != (int64_t)Hkv * D))) ||
+        (v && v == v_out && (slot || (!one && v_stride != (int64_t)Hkv * D))))
+        return QSA_ERR_INVALID_ARG;
     int sms = 0;
     qsa_status_t st = current_device(&sms);
     if (st != QSA_OK) return st;

@@ -471,8 +471,9 @@ QSA_API qsa_status_t qsa_rope(const void *x, int64_t x_stride, void *y, int64_t 
  *          negative one leaves both caches as they are; one >= L_max does too and
  *          is recorded as QSA_ERR_DEVICE.  NULL: row t, and L_max must be T.
  *   ws     NULL, or a workspace whose first 256 bytes take the status word
- * q_out may be q (k_out k, v_out v) where the layouts agree.  D, rot and positions
- * as in qsa_rope.  T == 0 is a no-op.
+ * q_out may be q (k_out k, v_out v without slots) where its tokens lie Hq * D (Hkv * D)
+ * apart; otherwise outputs do not overlap inputs.  D, rot and positions as in qsa_rope.
+ * T == 0 is a no-op.
  */
 QSA_API qsa_status_t qsa_qk_norm_rope(
     const qsa_bf16_t *q, int64_t q_stride, const qsa_bf16_t *k, int64_t k_stride,

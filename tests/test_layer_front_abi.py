@@ -156,3 +156,19 @@ def test_sparse_tree_stages_fit_32_bits(lib, Hq, Hkv, D, most):
     assert call(B=most + 1, bud=2048) == WORKSPACE  # fewer stages a row
     # the size function, which is not told Hkv, has none where no Hkv fits
     assert size(230000, 256, Hq, D, 4, 4096) == SIZE_MAX
+
+
+def test_norm_rope_in_place_where_the_layouts_agree_only(lib):
+    """Rows written elsewhere than where they were read would be read again: a strided input,
+    or slots, in place."""
+    at = lambda i: ctypes.c_void_p(0x10000 * (i + 1))
+    names = ("q qs k ks v vs B T Hq Hkv D qw kw eps f rot lay m pos pos0 qo ko vo slot L ws "
+             "s").split()
+    good = dict(q=at(0), qs=2048, k=at(1), ks=256, v=at(2), vs=256, B=2, T=3, Hq=16, Hkv=2, D=128,
+                qw=F, kw=F, eps=1e-6, f=F, rot=128, lay=0, m=1.0, pos=None, pos0=None, qo=at(3),
+                ko=at(4), vo=at(5), slot=None, L=3, ws=None, s=None)
+    call = _caller(lib.qsa_qk_norm_rope, names, good)
+    for kw in (dict(qo=at(0), qs=2560), dict(ko=at(1), ks=2560), dict(vo=at(2), vs=2560),
+               dict(ko=at(1), slot=F), dict(vo=at(2), slot=F), dict(ko=at(1), slot=F, L=9),
+               dict(ko=at(1), slot=F, B=1, T=1)):
+        assert call(**kw) == INVALID, kw
