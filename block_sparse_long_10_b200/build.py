@@ -4,11 +4,12 @@ Each ``csrc/*.cu`` file is compiled to an object under ``_build/`` (in
 parallel, skipped when up to date) and linked, with the CUDA runtime linked
 statically, into ``block_sparse_long_10_b200/libqsa.so``.  ``csrc/bind.cpp``, the
 native part of the Python binding, becomes ``_bind.so`` beside it (g++, against
-torch's headers).
+torch's headers; left out where there is no torch with CUDA).
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import contextlib
 import glob
 import os
 import subprocess
@@ -22,6 +23,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqsa.so")
 BIND_SRC = os.path.join(CSRC, "bind.cpp")
 BIND = os.path.join(PKG, "_bind.so")
+BIND_STAMP = os.path.join(BUILD, "bind.stamp")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + [
@@ -70,10 +72,42 @@ def build(verbose: bool = False, extra: list[str] | None = None, force: bool = F
     if not (os.path.exists(LIB)
             and os.path.getmtime(LIB) >= max(os.path.getmtime(o) for o in objs)):
         _link([_nvcc(), *ARCH, "-shared", "-cudart", "static", *objs], LIB, verbose)
-    newest = max(os.path.getmtime(f) for f in (BIND_SRC, os.path.join(ROOT, "include", "qsa.h")))
-    if not (os.path.exists(BIND) and os.path.getmtime(BIND) >= newest):
-        _link(_bind_cmd(), BIND, verbose)
+    _build_bind(verbose)
     return LIB
+
+
+def _build_bind(verbose: bool) -> None:
+    """The Python binding's native part, where there is a CUDA build of torch to make it
+    against (the C library does not need one); made again when that torch, or the Python,
+    is another one."""
+    made_for = _bind_made_for()
+    newest = max(os.path.getmtime(f) for f in (BIND_SRC, os.path.join(ROOT, "include", "qsa.h")))
+    if os.path.exists(BIND) and os.path.getmtime(BIND) >= newest and made_for is not None:
+        with contextlib.suppress(FileNotFoundError), open(BIND_STAMP) as f:
+            if f.read() == made_for:
+                return
+    if made_for is None:
+        print(f"{BIND} is not built: no torch with CUDA", file=sys.stderr)
+        with contextlib.suppress(FileNotFoundError):
+            os.remove(BIND)  # one for another torch does not load, or worse
+        return
+    _link(_bind_cmd(), BIND, verbose)
+    with open(BIND_STAMP, "w") as f:
+        f.write(made_for)
+
+
+def _bind_made_for() -> str | None:
+    """The torch and Python that a binding built now is for; None without a usable torch."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    home = os.path.dirname(torch.__file__)
+    for f in ("include/c10/cuda/CUDAStream.h", "lib/libc10_cuda.so", "lib/libtorch_python.so"):
+        if not os.path.exists(os.path.join(home, f)):
+            return None
+    return (f"{torch.__version__} cxx11abi={int(torch._C._GLIBCXX_USE_CXX11_ABI)} "
+            f"{sysconfig.get_config_var('SOABI')}")
 
 
 def _link(cmd: list[str], out: str, verbose: bool) -> None:
