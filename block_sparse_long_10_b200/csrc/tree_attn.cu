@@ -262,8 +262,9 @@ QSA_DEVICE float max3(float a, float b, float c) {
 
 // 2^x for two x <= 2^7 on the FMA pipe: x = j + f with j whole and |f| <= 1/2 (adding 1.5 * 2^23
 // rounds to j and leaves it in the low bits), 2^f by a polynomial of degree 5 fitted to the
-// least largest relative error with 2^0 = 1 exactly (2^-22.6 after fp32's rounding; the
-// exponential unit's is 2^-22), j added to the exponent.  0 from x = -127 on.
+// least largest relative error with 2^0 = 1 exactly (below 2^-22.4 over every fp32 f; the
+// exponential unit's is 2^-22), j added to the exponent.  From x = -126 down, where fp32 has no
+// more exponents, some value up to 2^-126, and 0 from x = -127 on.
 QSA_DEVICE void exp2_fma(uint64_t x2, float &p0, float &p1) {
     constexpr float SHIFT = 12582912.f;
     float x0, x1;
