@@ -27,7 +27,8 @@ namespace rope {
 constexpr int THREADS = 256;
 // The plain rotation: vectors of 4 (with 8, in bf16, 98 registers a thread left two blocks an SM:
 // 8 x 900 tokens of 16 heads of 128 15.0 us, with 4 13.0), and head rows whose loads are issued
-// together.
+// together.  On tensors that are not in L2 that call is 14.4 us, 32K tokens are 47 us: 1.6 and
+// 1.15 times the time of their bytes at a copy's rate; the short one's rest is its launch.
 constexpr int ROPE_VEC = 4;
 template <typename T>
 constexpr int ROPE_ROWS = sizeof(T) == 4 ? 2 : 4;
@@ -224,9 +225,10 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const RopeArgs a) {
 // one batch, and enough bytes are in flight for HBM whatever the occupancy.  What bounds
 // the kernels beyond that is the issue of instructions: so D is a template argument and
 // the batches are unrolled (offsets are immediates), and the arithmetic is in packed pairs
-// of fp32.  32K tokens, 16 + 2 heads of 128, forward / backward with fp32 gradients: rows
-// from registers 84 / 195 us, a ring of single rows 66 / 164 us, this 61 / 134 us (5.5 and
-// 5.6 TB/s of a copy's 6.5).
+// of fp32.  32K tokens, 16 + 2 heads of 128, forward / backward with fp32 gradients, a few
+// calls at the full clock: rows from registers 84 / 195 us, a ring of single rows 66 / 164 us,
+// this 62.5 / 134 us (5.4 and 5.6 TB/s of a copy's 6.5).  Call after call for a second, the power
+// limit takes the clock to 1.85 / 1.75 GHz and the calls to 66 / 138 us.
 
 // Packed fp32 pairs.
 struct F2 {
@@ -816,8 +818,9 @@ __global__ void __launch_bounds__(1024)
 int pick_vec(int rot) { return rot % 16 == 0 ? 8 : 4; }
 
 // Heads per item of the plain rotation: a token's heads share one set of angles, but at most
-// `most` (2 x 4099 tokens of 16 heads of 128 in fp32: 23.3 us with 2, 23.7 with 4, 25.2 with
-// 8), and a small batch is spread over more lanes first.  (Through the ring below it took
+// `most` (2 x 4099 tokens of 16 heads of 128 in fp32: 31.0 us with 1, 25.1 with 2 and 4, 25.9
+// with 8; 32K tokens in bf16 109 with 1, 64.6 with 2, 47.2 with 4, 45.7 with 8), and a small
+// batch is spread over more lanes first.  (Through the ring below it took
 // 37 us: without the norms' arithmetic there is nothing for a ring to hide.)
 int heads_per_item(int64_t n_tok, int rows, int most, int lanes, int num_sms) {
     const int64_t want = (int64_t)num_sms * 1024 / lanes;  // groups that fill the GPU
@@ -828,8 +831,8 @@ int heads_per_item(int64_t n_tok, int rows, int most, int lanes, int num_sms) {
 
 // Batches of rows per item, up to three, which share one set of angles: what makes the fewest
 // rounds of the resident groups, each as long as its batches and the angles (`angles`, in
-// batches).  32K tokens of 6 batches: 61 us with 3, 65 with 2 (more angles) and 65 with all 6
-// (a last round that is half empty); 4000 tokens 13.7 us with 3, 16.5 with 1.
+// batches).  32K tokens of 6 batches: 62.5 us with 3, 67 with 2 (more angles) and 66 with all 6
+// (a last round that is half empty), 81 with 1; 4000 tokens 14.9 us with 3, 18.5 with 1.
 int batches_per_item(int64_t n_tok, int batches, int64_t groups, double angles) {
     int best = 1;
     double least = 0;
@@ -845,7 +848,7 @@ int batches_per_item(int64_t n_tok, int batches, int64_t groups, double angles) 
 }
 
 // Threads of a block: 256, or fewer while that leaves SMs without one (64 sequences' decode
-// step: 4.1 us with 64 threads a block, 5.4 with 256).
+// step: 6.16 us with 64 or 128 threads a block, 6.42 with 256).
 int block_of(int64_t items, int lanes, int num_sms) {
     int t = THREADS;
     while (t > 64 && items * lanes < (int64_t)num_sms * t) t /= 2;

@@ -38,13 +38,18 @@ constexpr float LN2 = 0.6931471805599453f;
 // rows' stages, in one row, are cut into equal runs, one per CTA; each row that a run meets
 // leaves a part.
 // (8 x 16 drafts, 2048 tokens each of 64K: 39 us for 144 MB from HBM and 268 MB gathered through
-// L2, 3.7 and 6.9 TB/s: rows share blocks but each fetches its own.)
+// L2, 3.7 and 6.9 TB/s: rows share blocks but each fetches its own, and more than half of what it
+// fetches is not in L2 yet; with one selection for a sequence's drafts 34 us, with a random one
+// for each 48.)
 enum Mode { PREFILL = 0, SPLIT = 1, TREE = 2 };
 
 // Prefill: 2-stage ring, 3 CTAs per SM (12 warps: the gather is latency-bound
 // and more resident warps beat a deeper ring).  Split decode: 3-stage ring,
 // 2 CTAs per SM (few items per SM, a deeper ring per item pays).  Trees run like
-// prefill: their rows are many short items that share blocks in L2.
+// prefill: where a step's drafts fill the SMs and share blocks, more CTAs beat a deeper ring; where
+// they share nothing or are few it is the other way, by less (calls, 2 stages x 3 CTAs / 3 x 2,
+// budget 2048 of 64K: 8 x 16 drafts 39.0 / 42.2 us, with one selection for all 33.8 / 39.8, with
+// random ones 48.1 / 47.5; 32 x 4 drafts 42.8 / 44.1; 8 x 4 19.5 / 18.7; 1 x 16 12.8 / 12.1).
 template <int MODE>
 struct Ring {
     static constexpr int STAGES = MODE == SPLIT ? 3 : 2;

@@ -92,14 +92,18 @@ struct Args {
 // stream's products run under the other's softmax.  P (bf16) overwrites the S it came
 // from.  O is rescaled only when the running maximum has grown by more than 8 (a
 // factor 256) since its last rescale: sums and O stay far inside fp32, and P keeps bf16's
-// relative precision at any size.  P is rounded to bf16 for the matrix product; the sum
-// is taken of the unrounded values, in fp32.
+// relative precision at any size.  P is rounded to bf16 for the matrix product, which takes
+// both operands in V's type: at most 2^-8 of each weight, unbiased, 0.0018 to 0.0023 of the
+// output's size against 64 bits where the output's own rounding is 0.0017.  The sum is taken of
+// the unrounded values, in fp32.
 //
 // What bounds it.  Up to 128 rows a unit: HBM (32 x 8 drafts over 8K to 16K: the CTAs' runs end
-// 48 to 66 us in, 409 MB; a call is 75 us of graph replays).  More: the chain of a stream's step,
+// 48 to 66 us in, 409 MB; a call is 77 us).  More: the chain of a stream's step,
 // softmax about 1500 clocks, its own two products 1024, handing over about 400, against 2048
 // of products for both streams (4 x 64 drafts over 64K: runs of 102 to 119 us, 137 GFLOP, the
-// tensor pipe 58 % busy at the 1.6 GHz that the power limit leaves; a call is 136 to 143 us).
+// tensor pipe 58 % busy; a call is 139 us).  These are a few calls (or graph replays, which take
+// as long) at 1.9 GHz; call after call for a second, the power limit takes the clock to 1.54
+// and 1.40 GHz and the calls to 81 and 168 us.
 constexpr int ATOM = KT * 128; // bytes of a 64-column half tile in shared memory
 constexpr int SOFT = 256;      // softmax threads
 constexpr int THREADS = SOFT + 96;   // and a producer, an MMA and a cleaning warp
@@ -457,7 +461,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    // the merge kernel may start on the chains
+    // The merge may be launched now: its blocks (no room beside this CTA's registers) are handed
+    // out as SMs fall free, and have their lengths and indices when the last run ends.
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     Walk<NT> walk;
     if (!walk.start(a, lane)) return;
@@ -995,24 +1000,33 @@ cudaError_t run_dense(const CUtensorMap &tk, const CUtensorMap &tv, const Args &
     return cudaGetLastError();
 }
 
-// 8 warps a (row, head) where all of them run at once (3 blocks on each of 148 SMs), and in two
-// rounds where a unit, as the grid is shared out, has 16 parts or more (whole call, 8 warps / a
-// warp: 448 pairs of 37 parts 24.7 / 29.0 us, 768 of 18 17.2 / 19.7, but 640 of 5 20.6 / 18.6
-// and 1280 of 18 43.2 / 41.9).  A group from two rounds of 24 warps an SM on, a warp between
-// (group / warp: 65536 pairs 44.5 / 67 us, 8192 30.8 / 33.7, 4096 76.0 / 74.6).  The group has
-// D / 8 lanes from two parts a unit on, else 8 (16 / 8 lanes: 8192 pairs of 5 parts 33.0 / 35.0
-// us, 32768 of one 28.8 / 26.8).
+// 8 warps a (row, head) where all of them run at once (3 blocks on each SM), and in two rounds
+// where a unit, as the grid is shared out, has 16 parts or more.  A group from two rounds of 24
+// warps an SM on, a warp between.  The group has D / 8 lanes from two parts a unit on, else 8.
+// Whole calls of dense trees, 16 heads, on three sets of tensors in turn (us; D = 128 / 64):
+//   pairs of parts   8 warps      a warp       D / 8 lanes  8 lanes
+//      112 of   8    12.3 / 11.2  12.6 / 11.3  13.0 / 12.3  14.8 / 12.3
+//      448 of  37    28.9 / 22.6  33.8 / 24.2  39.8 / 28.9  57.6 / 28.9
+//      768 of  18    17.5 / 16.4  19.0 / 14.5  22.3 / 18.1  32.5 / 18.1
+//      640 of   5    22.5 / 18.5  20.9 / 16.4  21.9 / 16.6  24.2 / 16.7   (8 heads)
+//     1280 of  18    22.6 / 20.5  22.5 / 18.5  26.5 / 20.5  37.0 / 20.5
+//     4096 of   9                  162 / 113    166 / 114    176 / 114
+//     8192 of   5                 38.7 / 39.7  35.5 / 33.9  38.2 / 33.6
+//    32768 of   1                 38.9 / 34.8  30.5 / 22.6  29.2 / 22.6
+// Sparse (a unit is a row, three CTAs an SM), D = 128: 256 pairs of 28 parts 12.7 us with 8 warps,
+// 16.0 with one; 640 of 22 22.3 and 22.4, with a budget of 512 13.9 and 15.3; 1280 of 6 30.2 and
+// 27.2.
 template <int D, bool SPARSE>
-cudaError_t run_merge(const Args &a, int ctas, cudaStream_t s) {
+cudaError_t run_merge(const Args &a, int ctas, int sms, cudaStream_t s) {
     const int64_t pairs = (int64_t)a.B * a.N * a.Hq;
     const int64_t units = (int64_t)a.B * (SPARSE ? a.N : a.Hkv * a.units);
     auto launch = [&](auto kern, int per) {
         return launch_dependent(kern, dim3((unsigned)((pairs + per - 1) / per)), dim3(256), 0, s, a);
     };
     constexpr int L = D / 8;
-    if (pairs <= 148 * (ctas >= 16 * units ? 6 : 3))
+    if (pairs <= (int64_t)sms * (ctas >= 16 * units ? 6 : 3))
         return launch(tree_merge_kernel<D, SPARSE, 8, L>, 1);
-    if (pairs <= 148 * 48) return launch(tree_merge_kernel<D, SPARSE, 1, L>, 8);
+    if (pairs <= (int64_t)sms * 48) return launch(tree_merge_kernel<D, SPARSE, 1, L>, 8);
     // (so many pairs of a sparse call have a part or two each)
     if constexpr (!SPARSE)
         if (ctas >= 2 * units) return launch(tree_merge_kernel<D, SPARSE, 0, L>, 8 * 32 / L);
@@ -1072,10 +1086,10 @@ cudaError_t launch_tree_decode(const uint16_t *q, const uint16_t *k, const uint1
                     : tree::run_dense<128, 1>(tk, tv, a, ctas, s);
     }
     if (e != cudaSuccess) return e;
-    if (sel) return D == 64 ? tree::run_merge<64, true>(a, ctas, s)
-                             : tree::run_merge<128, true>(a, ctas, s);
-    return D == 64 ? tree::run_merge<64, false>(a, ctas, s)
-                   : tree::run_merge<128, false>(a, ctas, s);
+    if (sel) return D == 64 ? tree::run_merge<64, true>(a, ctas, sms, s)
+                            : tree::run_merge<128, true>(a, ctas, sms, s);
+    return D == 64 ? tree::run_merge<64, false>(a, ctas, sms, s)
+                   : tree::run_merge<128, false>(a, ctas, sms, s);
 }
 
 }  // namespace qsa
