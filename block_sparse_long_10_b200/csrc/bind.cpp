@@ -10,6 +10,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <initializer_list>
 #include <string>
@@ -167,7 +168,8 @@ struct Freq {
         const at::Tensor &t = tensor(o, "freq");
         of_rank(t, 1, "freq");
         p = need<double>(o, F64, t.sizes(), dev, "freq");
-        rot = 2 * (int)t.numel();
+        // (more pairs than any head has are refused by the call, however many)
+        rot = 2 * (int)std::min<int64_t>(t.numel(), 1 << 20);
     }
 };
 

@@ -153,3 +153,14 @@ def test_every_call_gives_the_same_bits(N, prefix, sparse):
     for _ in range(30):
         o, lse, _ = _run(x, sel, 2048)
         assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+
+
+def test_frequency_tables_of_any_length_are_refused():
+    """Longer than a head's pairs, to where twice the count no longer fits 32 bits."""
+    x = torch.zeros(1, 2, 1, 64, dtype=BF, device=DEV)
+    for n in (33, 1 << 21, 1 << 30, 1 << 31):
+        table = torch.empty(n, dtype=torch.float64, device=DEV)  # (17 GB at most, never read)
+        with pytest.raises(qsa.QSAError):
+            qsa.qsa_rope(x, torch.empty_like(x), table)
+        del table
+    torch.cuda.empty_cache()
