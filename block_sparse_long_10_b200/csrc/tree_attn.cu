@@ -93,9 +93,9 @@ struct Args {
 // from.  O is rescaled only when the running maximum has grown by more than 8 (a
 // factor 256) since its last rescale: sums and O stay far inside fp32, and P keeps bf16's
 // relative precision at any size.  P is rounded to bf16 for the matrix product, which takes
-// both operands in V's type: at most 2^-8 of each weight, unbiased, 0.0018 to 0.0023 of the
-// output's size against 64 bits where the output's own rounding is 0.0017.  The sum is taken of
-// the unrounded values, in fp32.
+// both operands in V's type: at most 2^-8 of each weight, unbiased: the output is off by 0.0018 to
+// 0.0026 of its size against 64 bits (2-norms), where its own rounding alone is 0.0017.  The sum
+// is taken of the unrounded values, in fp32.
 //
 // What bounds it.  Up to 128 rows a unit: HBM (32 x 8 drafts over 8K to 16K: the CTAs' runs end
 // 48 to 66 us in, 409 MB; a call is 77 us).  More: the chain of a stream's step,
