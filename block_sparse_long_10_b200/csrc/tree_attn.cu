@@ -96,6 +96,9 @@ struct Args {
 // both operands in V's type: at most 2^-8 of each weight, unbiased: the output is off by 0.0018 to
 // 0.0026 of its size against 64 bits (2-norms), where its own rounding alone is 0.0017.  The sum
 // is taken of the unrounded values, in fp32.
+// (Two streams over one tensor core, rescaling past a threshold only and a polynomial for part of
+// the exponentials are published ideas for attention on this architecture; layout, split,
+// thresholds and coefficients are this file's.)
 //
 // What bounds it.  Up to 128 rows a unit: HBM (32 x 8 drafts over 8K to 16K: the CTAs' runs end
 // 48 to 66 us in, 409 MB; a call is 77 us).  More: the chain of a stream's step,
